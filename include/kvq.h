@@ -454,6 +454,137 @@ KVQ_API kvq_status kvq_set_wait_limit(int64_t cycles);
  */
 KVQ_API kvq_status kvq_set_launch_stamps(void *buf, int32_t n_slots, int32_t ctas_per_slot);
 
+/*
+ * ---------------------------------------------------------------------------------
+ * Paged cache: the rows of many sequences in one pool of fixed-size pages, for serving
+ * batches whose sequences come, grow and go.  Append (with the rotary position embedding on
+ * the way), attention (single tokens, drafts and prompt chunks alike) and gather share one
+ * cache format and one batch description.  Multi-session stacking of resident sequences is
+ * "HAL #582 -- per-layer KV compression study", section 4; pages and block tables are this
+ * library's own.
+ *
+ * Pool layout.  [n_pages][Hkv][page_size / 16] tile records; a record holds 16 consecutive
+ * rows of one KV head: K codes, V codes, K scales, V scales (each NS = D / 128 slices, laid
+ * out inside as in the tiles of the contiguous cache above; no scales for f16).  K/V types:
+ * f16/f16, q8_0/q8_0, q8_0/q4_0 and q4_0/q4_0.  Position t of a sequence is row t % page_size
+ * of page block_table[t / page_size]; a page may appear in several block tables (a shared
+ * prefix) as long as no call appends to it while another call uses it.
+ *
+ * Ownership, streams, errors.  As for the contiguous cache: the caller owns the pool and the
+ * state block (16 bytes, zeroed before kvq_paged_create; it holds only the error word), calls
+ * enqueue and return, and argument errors are reported before any launch.  The handle keeps no
+ * lengths and is not written by append, gather or attention, so calls that read the pool may
+ * run at the same time on several streams, each with its own workspace; an append must be
+ * ordered against calls that use the pages it writes.  The handle's device must be current.
+ */
+typedef struct {
+    int32_t n_pages;    /* pages in the pool (>= 1)                                    */
+    int32_t page_size;  /* rows per page; a positive multiple of 16                    */
+    int32_t n_kv_heads; /* Hkv (>= 1)                                                  */
+    int32_t head_dim;   /* D: 128 or 256                                               */
+    int32_t type_k;     /* kvq_type of the K rows                                      */
+    int32_t type_v;     /* kvq_type of the V rows                                      */
+} kvq_paged_desc;
+
+typedef struct kvq_paged kvq_paged; /* opaque host handle */
+
+/* Element type of activations (keys, values, queries and outputs). */
+typedef enum { KVQ_DT_F32 = 0, KVQ_DT_F16 = 1, KVQ_DT_BF16 = 2 } kvq_dtype;
+
+/*
+ * The sequences of one call.  Tokens of all sequences are packed: sequence b has the tokens
+ * cu_q[b] .. cu_q[b + 1] - 1 (cu_q NULL: one token each, token b), which are its last
+ * positions lens[b] - n_b .. lens[b] - 1, n_b = cu_q[b + 1] - cu_q[b].  lens counts them: an
+ * append and the attention after it take the same batch.  Tokens of a negative position
+ * (n_b > lens[b]) are not written and attend to nothing.  Tokens from cu_q[n_seqs] to
+ * n_tokens - 1 are padding: never read and their outputs never written.
+ * The three arrays are device memory and are read when the kernels run, so a captured call
+ * follows their contents at replay; n_seqs, n_tokens, max_q, max_len and the pointers are
+ * fixed at the call.  A sequence whose entries contradict the call (n_b negative or above
+ * max_q, tokens past n_tokens, a length below 0 or above max_len) is skipped and sets
+ * KVQ_DEVERR_BATCH; so does a page number outside the pool, whose rows are neither written
+ * nor attended to (gather gives zeros).
+ */
+typedef struct {
+    int32_t n_seqs;             /* sequences (0: the call does nothing)                     */
+    int32_t n_tokens;           /* rows of k, v, q and the outputs                          */
+    int32_t max_q;              /* most tokens any sequence has in this call (>= 1)         */
+    int32_t max_len;            /* most positions any sequence has; at most table_width * page_size */
+    const int32_t *cu_q;        /* [n_seqs + 1] or NULL                                     */
+    const int32_t *lens;        /* [n_seqs]                                                 */
+    const int32_t *block_table; /* [n_seqs][table_stride], entries 0 .. table_width - 1 used */
+    int32_t table_width, table_stride;
+} kvq_paged_batch;
+
+/* A sequence's entries contradict the call, or a page number or a position's angles are
+ * missing (see kvq_paged_batch and kvq_rope); the rest of the call is unaffected. */
+#define KVQ_DEVERR_BATCH 0x4
+
+/* Bytes of the pool and of the state block.  Pure host arithmetic; no CUDA call. */
+KVQ_API kvq_status kvq_paged_size(const kvq_paged_desc *desc, size_t *pool_bytes, size_t *state_bytes);
+/* Create a handle over the caller's pool and zeroed state block (both 16-byte aligned, memory
+ * of the current device).  No CUDA work is enqueued. */
+KVQ_API kvq_status kvq_paged_create(const kvq_paged_desc *desc, void *pool, void *state, kvq_paged **out);
+KVQ_API kvq_status kvq_paged_destroy(kvq_paged *cache);
+/* Read and clear the device error word (synchronises `stream`).  *h_err = KVQ_DEVERR_* bits. */
+KVQ_API kvq_status kvq_paged_read_error(kvq_paged *cache, void *stream, int32_t *h_err);
+
+/*
+ * Rotary position embedding.  cos_sin: fp32 [n_positions][rot_dim], per position the cosines
+ * of its rot_dim / 2 angles, then the sines.  The first rot_dim values of a head are rotated
+ * in pairs (a, b) -> (a cos - b sin, b cos + a sin), in fp32 with one rounding per operation;
+ * the rest pass through.  Pair j is (j, j + rot_dim / 2), or (2j, 2j + 1) when interleaved.
+ * The angle row of a token is its position in the sequence, or positions[token] (device int32
+ * [n_tokens]) when given; a token whose row is outside the table is skipped and sets
+ * KVQ_DEVERR_BATCH.  rot_dim: a positive multiple of 8, at most head_dim.
+ */
+typedef struct {
+    const float *cos_sin;
+    const int32_t *positions; /* or NULL */
+    int32_t n_positions, rot_dim, interleaved;
+} kvq_rope;
+
+/*
+ * Append: rotate the keys (rope non-NULL), quantise keys and values by the rules above and
+ * write them into their pages.  k and v: [n_tokens][Hkv][D] of type dtype, consecutive tokens
+ * k_stride / v_stride elements apart (heads and values contiguous; at least Hkv * D, a
+ * multiple of 8), so that slices of a fused projection can be passed.  With q non-NULL the
+ * queries [n_tokens][n_q_heads][D] (stride q_stride) are rotated by the same angles into
+ * q_out (stride q_out_stride; q_out may be q itself with the same stride) in dtype, rounded
+ * once.  rope NULL appends unrotated rows (q must then be NULL).  One launch.
+ * Other rows of the pool are left as they were.
+ */
+KVQ_API kvq_status kvq_paged_append(kvq_paged *cache, const kvq_paged_batch *batch, const void *k, const void *v,
+                                    kvq_dtype dtype, int64_t k_stride, int64_t v_stride, const kvq_rope *rope,
+                                    const void *q, int32_t n_q_heads, int64_t q_stride, void *q_out,
+                                    int64_t q_out_stride, void *stream);
+
+/*
+ * Gather: the values of the batch's rows, k_out and v_out [n_tokens][Hkv][D] of type dtype
+ * (rounded once from the exact scale * code).  With n_b = lens[b] whole sequences are read.
+ * Tokens of a negative position give zeros.  One launch.
+ */
+KVQ_API kvq_status kvq_paged_gather(const kvq_paged *cache, const kvq_paged_batch *batch, void *k_out, void *v_out,
+                                    kvq_dtype dtype, void *stream);
+
+/*
+ * Causal grouped-query attention of the batch's tokens over their sequences' pages: token i of
+ * sequence b (position p = lens[b] - n_b + i) attends to positions 0 .. p, which must have been
+ * appended before.
+ *   q    : [n_tokens][n_q_heads][D] of type dtype, tokens q_stride elements apart
+ *   out  : [n_tokens][n_q_heads][D] of type dtype, contiguous; a token that attends to nothing
+ *          gets 0
+ *   lse  : fp32 [n_tokens][n_q_heads], natural log (-inf where nothing is attended), or NULL
+ *   workspace: kvq_paged_attention_workspace_size bytes for the same batch sizes; needs no
+ *          initialisation and keeps nothing between calls.
+ * n_q_heads: a multiple of Hkv.  fp32 queries: max_q at most KVQ_MAX_VERIFY_QUERIES.
+ */
+KVQ_API kvq_status kvq_paged_attention_workspace_size(const kvq_paged *cache, const kvq_paged_batch *batch,
+                                                      int32_t n_q_heads, kvq_dtype dtype, size_t *bytes);
+KVQ_API kvq_status kvq_paged_attention(const kvq_paged *cache, const kvq_paged_batch *batch, const void *q,
+                                       kvq_dtype dtype, int32_t n_q_heads, int64_t q_stride, float scale,
+                                       void *workspace, size_t workspace_bytes, void *out, float *lse, void *stream);
+
 KVQ_API const char *kvq_status_string(kvq_status status);
 KVQ_API int32_t kvq_abi_version(void);
 

@@ -26,7 +26,10 @@ CODE_TILE = {F16: 4096, Q8_0: 2048, Q4_0: 1024, Q4_1: 1024, Q5_0: 1280, Q5_1: 12
 TYPE_NAMES = {v: k for k, v in TYPE_IDS.items()}
 STATUS = {0: "KVQ_OK", 1: "KVQ_ERR_INVALID_ARG", 2: "KVQ_ERR_UNSUPPORTED", 3: "KVQ_ERR_CAPACITY",
           4: "KVQ_ERR_ALIGNMENT", 5: "KVQ_ERR_CUDA", 6: "KVQ_ERR_DEVICE", 7: "KVQ_ERR_SCRATCH"}
-DEVERR_CAPACITY, DEVERR_TIMEOUT = 0x1, 0x2
+DEVERR_CAPACITY, DEVERR_TIMEOUT, DEVERR_BATCH = 0x1, 0x2, 0x4
+# element types of activations (kvq_dtype)
+DTYPE_IDS = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+MAX_F32_QUERIES = 16  # KVQ_MAX_VERIFY_QUERIES: fp32 queries per sequence of a paged attention call
 
 
 class KvqError(RuntimeError):
@@ -45,11 +48,27 @@ class Desc(ctypes.Structure):
                 ("capacity", ctypes.c_int32), ("type_k", ctypes.c_int32), ("type_v", ctypes.c_int32)]
 
 
+class PagedDesc(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("type_k", ctypes.c_int32), ("type_v", ctypes.c_int32)]
+
+
+class PagedBatch(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("n_tokens", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("max_len", ctypes.c_int32), ("cu_q", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("table_width", ctypes.c_int32), ("table_stride", ctypes.c_int32)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("n_positions", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libkvq.so not built ({LIB_PATH}); run `python quantised_kv_long_gb300/build.py` or __graft_entry__.build()")
     L = ctypes.CDLL(LIB_PATH)
-    vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     pdesc = ctypes.POINTER(Desc)
     sigs = {
         "kvq_cache_size": [pdesc, ctypes.POINTER(sz), ctypes.POINTER(sz), ctypes.POINTER(sz)],
@@ -73,6 +92,14 @@ def _load():
         "kvq_window_workspace_size": [vp, vp, i32, ctypes.POINTER(sz)],
         "kvq_window_decode": [vp, vp, vp, i32, ctypes.c_float, vp, vp, vp, vp],
         "kvq_window_append_decode": [vp, vp, vp, vp, vp, i32, ctypes.c_float, vp, vp, vp, vp],
+        "kvq_paged_size": [vp, ctypes.POINTER(sz), ctypes.POINTER(sz)],
+        "kvq_paged_create": [vp, vp, vp, ctypes.POINTER(vp)],
+        "kvq_paged_destroy": [vp],
+        "kvq_paged_read_error": [vp, vp, ctypes.POINTER(i32)],
+        "kvq_paged_append": [vp, vp, vp, vp, i32, i64, i64, vp, vp, i32, i64, vp, i64, vp],
+        "kvq_paged_gather": [vp, vp, vp, vp, i32, vp],
+        "kvq_paged_attention_workspace_size": [vp, vp, i32, i32, ctypes.POINTER(sz)],
+        "kvq_paged_attention": [vp, vp, vp, i32, i32, i64, ctypes.c_float, vp, sz, vp, vp, vp],
     }
     for name, args in sigs.items():
         fn = getattr(L, name)
@@ -396,3 +423,210 @@ def combine(part_o, part_m, part_l, out=None, lse=None, stream=None):
     _check(lib.kvq_combine(_ptr(part_o), _ptr(part_m), _ptr(part_l), rows, S, D, _ptr(out), _ptr(lse),
                            _stream(stream)), "kvq_combine")
     return out, lse
+
+
+# ---- paged cache ----
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def paged_size(n_pages, page_size, n_kv_heads, head_dim, type_k, type_v):
+    """(pool_bytes, state_bytes) of a paged cache (kvq_paged_size); pure host arithmetic."""
+    d = PagedDesc(n_pages, page_size, n_kv_heads, head_dim, _tid(type_k), _tid(type_v))
+    pb, sb = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib.kvq_paged_size(ctypes.byref(d), ctypes.byref(pb), ctypes.byref(sb)), "kvq_paged_size")
+    return pb.value, sb.value
+
+
+class Rope:
+    """Angles of the rotary position embedding for PagedCache.append (kvq_rope): `cos_sin` is a
+    contiguous fp32 CUDA tensor [n_positions, rot_dim] (cosines, then sines)."""
+
+    def __init__(self, cos_sin, interleaved=False):
+        _need(cos_sin.dtype == torch.float32 and cos_sin.is_contiguous() and cos_sin.dim() == 2 and cos_sin.is_cuda,
+              "cos_sin: a contiguous fp32 CUDA tensor [n_positions, rot_dim]")
+        self.cos_sin, self.interleaved = cos_sin, bool(interleaved)
+
+    @classmethod
+    def from_base(cls, n_positions, rot_dim, base=10000.0, interleaved=False, device=None):
+        """Angles position * base^(-2 j / rot_dim), j < rot_dim / 2, evaluated in 64 bits."""
+        j = torch.arange(rot_dim // 2, dtype=torch.float64, device=device or "cuda")
+        a = torch.arange(n_positions, dtype=torch.float64, device=j.device)[:, None] * base ** (-2.0 * j / rot_dim)
+        return cls(torch.cat([a.cos(), a.sin()], -1).float().contiguous(), interleaved)
+
+
+class PagedCache:
+    """A pool of pages for the rows of many sequences (kvq_paged_*).  `block_table` [n_seqs,
+    width] and `lens` [n_seqs] are int32 CUDA tensors that the caller keeps; `lens` counts the
+    tokens of the call.  Packed tokens: sequence b has rows cu_q[b] .. cu_q[b + 1] - 1 (cu_q
+    int32 [n_seqs + 1]), or one row each when cu_q is None.  max_q bounds the tokens of a
+    sequence (default: all of them), max_len its length (default: the table's width).
+
+    Work is enqueued on the current stream of the cache's device, or with `stream` as if that
+    stream were current (tensors made in the call belong to it)."""
+
+    def __init__(self, n_pages, page_size, n_kv_heads, head_dim, type_k="q8_0", type_v="q8_0", device=None):
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = n_pages, page_size, n_kv_heads, head_dim
+        self.type_k, self.type_v = type_k, type_v
+        pool_bytes, state_bytes = paged_size(n_pages, page_size, n_kv_heads, head_dim, type_k, type_v)
+        self.pool = torch.empty(pool_bytes, dtype=torch.uint8, device=self.device)
+        self.state = torch.zeros(state_bytes // 4, dtype=torch.int32, device=self.device)
+        self.desc = PagedDesc(n_pages, page_size, n_kv_heads, head_dim, _tid(type_k), _tid(type_v))
+        h = ctypes.c_void_p()
+        with torch.cuda.device(self.device):
+            # the state block is zeroed on this stream; other streams may use the cache at once
+            torch.cuda.current_stream().synchronize()
+            _check(lib.kvq_paged_create(ctypes.byref(self.desc), _ptr(self.pool), _ptr(self.state), ctypes.byref(h)),
+                   "kvq_paged_create")
+        self.handle = h
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h is not None and h.value:
+            lib.kvq_paged_destroy(h)
+            self.handle = None
+
+    def _batch(self, block_table, lens, cu_q, max_q, max_len, n_tokens):
+        n_seqs = lens.numel()
+        _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == n_seqs and
+              block_table.stride(1) == 1 and block_table.device == self.device, "block_table: int32 [n_seqs, width] on the cache's device")
+        _need(lens.dtype == torch.int32 and lens.is_contiguous() and lens.device == self.device,
+              "lens: contiguous int32 [n_seqs] on the cache's device")
+        if cu_q is None:
+            _need(n_tokens >= n_seqs, "without cu_q every sequence has one token")
+            max_q = 1
+        else:
+            _need(cu_q.dtype == torch.int32 and cu_q.is_contiguous() and cu_q.numel() == n_seqs + 1 and
+                  cu_q.device == self.device, "cu_q: contiguous int32 [n_seqs + 1] on the cache's device")
+            max_q = max(1, n_tokens) if max_q is None else max_q
+        width = block_table.shape[1]
+        return PagedBatch(n_seqs, n_tokens, max_q, width * self.page_size if max_len is None else max_len,
+                          0 if cu_q is None else cu_q.data_ptr(), lens.data_ptr(), block_table.data_ptr(), width,
+                          max(width, block_table.stride(0)))
+
+    def _rows(self, t, heads, what, dtype=None):
+        """Packed rows [n_tokens, heads, D] with contiguous heads and values: (pointer, token stride)."""
+        _need(t.device == self.device and t.dim() == 3 and t.shape[2] == self.head_dim and (heads is None or t.shape[1] == heads) and
+              t.dtype in DTYPE_IDS and (dtype is None or t.dtype == dtype), f"{what}: [n_tokens, heads, {self.head_dim}] of one activation type on the cache's device")
+        width = t.shape[1] * self.head_dim
+        _need(t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == self.head_dim), f"{what}: heads and values must be contiguous")
+        return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else width)
+
+    def _call(self, stream, fn, *args):
+        """fn(*args) with the cache's device, and `stream` if given, current."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return fn(*args)
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                return fn(*args)
+        return fn(*args)
+
+    def append(self, k, v, block_table, lens, cu_q=None, max_q=None, max_len=None, rope=None, positions=None, q=None,
+               q_out=None, stream=None):
+        """Rotate (rope) and quantise k, v [n_tokens, Hkv, D] into their pages.  With q
+        [n_tokens, Hq, D] also returns the rotated queries (q_out, which may be q)."""
+        return self._call(stream, self._append, k, v, block_table, lens, cu_q, max_q, max_len, rope, positions, q, q_out)
+
+    def _append(self, k, v, block_table, lens, cu_q, max_q, max_len, rope, positions, q, q_out):
+        kp, ks = self._rows(k, self.n_kv_heads, "k")
+        vp, vs = self._rows(v, self.n_kv_heads, "v", k.dtype)
+        n = k.shape[0]
+        _need(v.shape[0] == n, "k and v have the same tokens")
+        batch = self._batch(block_table, lens, cu_q, max_q, max_len, n)
+        ra, qp, qs, qop, qos, hq = None, 0, 0, 0, 0, 0
+        if rope is not None:
+            _need(rope.cos_sin.device == self.device, "rope: on the cache's device")
+            if positions is not None:
+                _need(positions.dtype == torch.int32 and positions.is_contiguous() and positions.numel() == n and
+                      positions.device == self.device, "positions: contiguous int32 [n_tokens] on the cache's device")
+            ra = ctypes.byref(RopeArgs(rope.cos_sin.data_ptr(), 0 if positions is None else positions.data_ptr(),
+                                       rope.cos_sin.shape[0], rope.cos_sin.shape[1], int(rope.interleaved)))
+        _need(rope is not None or positions is None, "positions are the rotation's")
+        result = None
+        if q is not None:
+            qp, qs = self._rows(q, None, "q", k.dtype)
+            _need(q.shape[0] == n, "q and k have the same tokens")
+            if rope is None:
+                _need(q_out is None, "q_out without a rotation")
+                result, qp, qs = q, 0, 0
+            else:
+                hq = q.shape[1]
+                result = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+                qop, qos = self._rows(result, hq, "q_out", k.dtype)
+                _need(result.shape[0] == n, "q_out and q have the same tokens")
+        _check(lib.kvq_paged_append(self.handle, ctypes.byref(batch), kp, vp, DTYPE_IDS[k.dtype], ks, vs, ra, qp, hq, qs, qop,
+                                    qos, torch.cuda.current_stream().cuda_stream), "kvq_paged_append")
+        return result
+
+    def gather(self, block_table, lens, n_tokens, cu_q=None, max_q=None, max_len=None, dtype=torch.float16, stream=None):
+        """The values of the batch's rows: (k, v), each [n_tokens, Hkv, D] of `dtype`.  Rows of
+        padding tokens are not written."""
+        return self._call(stream, self._gather, block_table, lens, n_tokens, cu_q, max_q, max_len, dtype)
+
+    def _gather(self, block_table, lens, n_tokens, cu_q, max_q, max_len, dtype):
+        _need(dtype in DTYPE_IDS, "dtype: float32, float16 or bfloat16")
+        batch = self._batch(block_table, lens, cu_q, max_q, max_len, n_tokens)
+        shape = (n_tokens, self.n_kv_heads, self.head_dim)
+        k = torch.empty(shape, dtype=dtype, device=self.device)
+        v = torch.empty(shape, dtype=dtype, device=self.device)
+        _check(lib.kvq_paged_gather(self.handle, ctypes.byref(batch), k.data_ptr(), v.data_ptr(), DTYPE_IDS[dtype],
+                                    torch.cuda.current_stream().cuda_stream), "kvq_paged_gather")
+        return k, v
+
+    def attention(self, q, block_table, lens, cu_q=None, max_q=None, max_len=None, scale=None, out=None, return_lse=False,
+                  workspace=None, stream=None):
+        """Causal attention of q [n_tokens, Hq, D] over the sequences' pages: out like q
+        (contiguous), and with return_lse also lse fp32 [n_tokens, Hq].  Rows of padding tokens
+        are not written.  `workspace`: a uint8 CUDA tensor of workspace_bytes(...) bytes used by
+        no other call at the same time (default: one made for this call)."""
+        return self._call(stream, self._attention, q, block_table, lens, cu_q, max_q, max_len, scale, out, return_lse, workspace)
+
+    def _attention(self, q, block_table, lens, cu_q, max_q, max_len, scale, out, return_lse, workspace):
+        qp, qs = self._rows(q, None, "q")
+        n, hq, d = q.shape
+        batch = self._batch(block_table, lens, cu_q, max_q, max_len, n)
+        dt = DTYPE_IDS[q.dtype]
+        if workspace is None:
+            workspace = torch.empty(self._workspace_bytes(batch, hq, dt), dtype=torch.uint8, device=self.device)
+        else:
+            _need(workspace.device == self.device and workspace.is_contiguous(), "workspace: contiguous, on the cache's device")
+        if out is None:
+            out = torch.empty((n, hq, d), dtype=q.dtype, device=self.device)
+        else:
+            _need(out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous() and out.device == self.device,
+                  "out: contiguous, like q")
+        lse = torch.empty((n, hq), dtype=torch.float32, device=self.device) if return_lse else None
+        _check(lib.kvq_paged_attention(self.handle, ctypes.byref(batch), qp, dt, hq, qs,
+                                       1.0 / math.sqrt(d) if scale is None else scale, workspace.data_ptr(),
+                                       workspace.numel() * workspace.element_size(), out.data_ptr(),
+                                       0 if lse is None else lse.data_ptr(), torch.cuda.current_stream().cuda_stream),
+               "kvq_paged_attention")
+        return (out, lse) if return_lse else out
+
+    def _workspace_bytes(self, batch, n_q_heads, dt):
+        b = ctypes.c_size_t()
+        _check(lib.kvq_paged_attention_workspace_size(self.handle, ctypes.byref(batch), n_q_heads, dt, ctypes.byref(b)),
+               "kvq_paged_attention_workspace_size")
+        return b.value
+
+    def workspace_bytes(self, n_seqs, n_tokens, n_q_heads, max_len, max_q=1, dtype=torch.bfloat16) -> int:
+        """Workspace of attention calls of these sizes (max_q tokens at most per sequence)."""
+        width = -(-max_len // self.page_size)
+        # the arrays' contents do not matter: any aligned address stands for them
+        batch = PagedBatch(n_seqs, n_tokens, max_q, max_len, 16 if max_q > 1 else 0, 16, 16, max(1, width), max(1, width))
+        return self._call(None, self._workspace_bytes, batch, n_q_heads, DTYPE_IDS[dtype])
+
+    def read_error(self, stream=None) -> int:
+        """Read and clear the device error word (DEVERR_* bits)."""
+        return self._call(stream, self._read_error)
+
+    def _read_error(self):
+        e = ctypes.c_int32()
+        _check(lib.kvq_paged_read_error(self.handle, torch.cuda.current_stream().cuda_stream, ctypes.byref(e)),
+               "kvq_paged_read_error")
+        return e.value
