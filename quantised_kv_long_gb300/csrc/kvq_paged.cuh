@@ -15,6 +15,7 @@ struct PagedView {
     const int32_t *cu_q, *lens, *table;
     int n_seqs, n_tokens, max_q, max_len, width, stride;
     int n_pages, page_tiles, Hkv;
+    int token0;  // without cu_q: the token of sequence 0
 };
 
 // One tile record: 16 rows of one KV head.  A record holds K and V together so that one bulk
@@ -39,7 +40,7 @@ struct PagedSeq {
 };
 __device__ __forceinline__ PagedSeq paged_seq(const PagedView &v, int b) {
     PagedSeq s;
-    s.first = v.cu_q ? __ldg(v.cu_q + b) : b;
+    s.first = v.cu_q ? __ldg(v.cu_q + b) : v.token0 + b;
     // the difference in 64 bits: entries may be any integers
     const long long n = v.cu_q ? static_cast<long long>(__ldg(v.cu_q + b + 1)) - s.first : 1;
     s.len = __ldg(v.lens + b);
@@ -84,6 +85,7 @@ struct Act<KVQ_DT_F32> {
     using type = float;
     static __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
     static __device__ __forceinline__ void store4(float *p, float4 x) { *reinterpret_cast<float4 *>(p) = x; }
+    static __device__ __forceinline__ void store2(float *p, float a, float b) { *reinterpret_cast<float2 *>(p) = make_float2(a, b); }
 };
 template <>
 struct Act<KVQ_DT_F16> {
@@ -96,6 +98,9 @@ struct Act<KVQ_DT_F16> {
     static __device__ __forceinline__ void store4(__half *p, float4 x) {
         *reinterpret_cast<uint2 *>(p) =
             make_uint2(h2_as_u32(__floats2half2_rn(x.x, x.y)), h2_as_u32(__floats2half2_rn(x.z, x.w)));
+    }
+    static __device__ __forceinline__ void store2(__half *p, float a, float b) {
+        *reinterpret_cast<uint32_t *>(p) = h2_as_u32(__floats2half2_rn(a, b));
     }
 };
 template <>
@@ -110,6 +115,9 @@ struct Act<KVQ_DT_BF16> {
         const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
         *reinterpret_cast<uint2 *>(p) =
             make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    }
+    static __device__ __forceinline__ void store2(__nv_bfloat16 *p, float a, float b) {
+        *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(a, b);
     }
 };
 
@@ -197,6 +205,11 @@ cudaError_t launch_paged_gather(int type_k, int type_v, int D, int dtype, const 
 cudaError_t launch_paged_attention(int type_k, int type_v, int D, int dtype, const PagedAttnParams &p, cudaStream_t s);
 // workspace bytes of a call; sizes known on the host only
 cudaError_t paged_attention_workspace(int type_k, int type_v, int D, int dtype, const PagedAttnParams &p, size_t *bytes);
+// few queries per sequence (kvq_paged_split.cuh), one translation unit per activation type
+cudaError_t launch_paged_split_f32(int type_k, int type_v, int D, const PagedAttnParams &p, cudaStream_t s);
+cudaError_t launch_paged_split_f16(int type_k, int type_v, int D, const PagedAttnParams &p, cudaStream_t s);
+cudaError_t launch_paged_split_bf16(int type_k, int type_v, int D, const PagedAttnParams &p, cudaStream_t s);
+cudaError_t paged_split_workspace(int D, size_t *bytes);
 
 // (K, V) type pairs of the paged cache
 constexpr bool is_paged_pair(int tk, int tv) {

@@ -93,9 +93,15 @@ cudaError_t attn_t(const PagedAttnParams &p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_paged_attention(int type_k, int type_v, int D, int dtype, const PagedAttnParams &p, cudaStream_t s) {
+    if (p.v.max_q <= KVQ_MAX_VERIFY_QUERIES) {
+        if (dtype == KVQ_DT_F32) return launch_paged_split_f32(type_k, type_v, D, p, s);
+        if (dtype == KVQ_DT_F16) return launch_paged_split_f16(type_k, type_v, D, p, s);
+        return launch_paged_split_bf16(type_k, type_v, D, p, s);
+    }
     KVQ_PAGED_DISPATCH(attn_t, (p, s))
 }
-cudaError_t paged_attention_workspace(int, int, int, int, const PagedAttnParams &, size_t *bytes) {
+cudaError_t paged_attention_workspace(int, int, int D, int, const PagedAttnParams &p, size_t *bytes) {
+    if (p.v.max_q <= KVQ_MAX_VERIFY_QUERIES) return paged_split_workspace(D, bytes);
     *bytes = 16;
     return cudaSuccess;
 }

@@ -84,7 +84,24 @@ def attend(q, k, v, scale):
     return out, lse, av, qk
 
 
-def bounds(out, av, qk, dtype, keys, dim, sixteen):
+def offset_terms(pair, q, k, v, scale, keys):
+    """What the offset of 4-bit codes adds to the errors: (scores [n, Hq], outputs).
+
+    A 4-bit value is d (c - 8), c in 0 .. 15, and a kernel may sum d c and 8 d apart and subtract: exact
+    products, but the two fp32 sums are up to 15 d and 8 d times their weights while their difference can
+    be 0.  With d <= max|x| / 8 over the rows, a sum of m such terms is off by at most
+    (m + 1) 2^-23 (15 + 8) / 8 max|x| times the sum of the weights: m = 32 (one block) with weights |q|
+    scale for the scores, m = keys with weights that sum to 1 for the outputs."""
+    hq = q.shape[1]
+    e = torch.zeros((q.shape[0], hq), dtype=torch.float64, device=q.device)
+    if keys == 0:
+        return e, 0.0
+    if pair[0] == "q4_0":
+        e = q.double().abs().sum(-1) * abs(scale) * float(k.abs().max()) * (23 / 8 * 33 * 2.0 ** -23)
+    return e, (float(v.abs().max()) * 23 / 8 * (keys + 1) * 2.0 ** -23 if pair[1] == "q4_0" else 0.0)
+
+
+def bounds(out, av, qk, dtype, keys, dim, sixteen, offset=None):
     """(bound of |out|'s error, bound of lse's) from the roundings the kernels may make.
 
     Scores: with `sixteen` (keys as 16-bit operands) each key value is rounded once, half a step of
@@ -92,12 +109,17 @@ def bounds(out, av, qk, dtype, keys, dim, sixteen):
     `dim` products add dim 2^-23 (products and partial sums).  A score off by e changes a weight by at most 2e
     relative (numerator and denominator), e < 1.  Weights and values as 16-bit operands: 2^-11 each for 16-bit
     outputs (and one product of weight and scale, 2^-11), 2^-19 otherwise.  fp32 sums over keys:
-    keys 2^-23 for numerator and denominator together.  Then half a step of the output's type."""
+    keys 2^-23 for numerator and denominator together.  Then half a step of the output's type.
+    `offset`: offset_terms(...) of 4-bit rows."""
     e = qk * ((2.0 ** -11 if sixteen else 2.0 ** -20) + dim * 2.0 ** -23) + 2.0 ** -20
+    if offset is not None:
+        e = e + offset[0]
     assert float(e.max()) < 0.5, "inputs too large for the first-order bound"
     part = 3 * 2.0 ** -11 if dtype != "f32" else 2.0 ** -19
     rel = 2 * e * (1 + 2 * e) + (part + keys * 2.0 ** -23)
     tol = out.abs() * HALF_STEP[dtype] + av * rel[..., None] * (1 + HALF_STEP[dtype])
     # values below the 16-bit types' normal range are rounded absolutely
     tol = tol + (2.0 ** -25 if dtype != "f32" else 2.0 ** -60)
+    if offset is not None:
+        tol = tol + offset[1]
     return tol, e + keys * 2.0 ** -23 + 2.0 ** -20

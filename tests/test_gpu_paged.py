@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from tests import kvq_layout
-from tests.paged_ref import DT, HALF_STEP, PAIRS, angles, attend, bounds, cumulative, dev, rotate, stored, table
+from tests.paged_ref import DT, PAIRS, angles, attend, bounds, cumulative, dev, offset_terms, rotate, stored, table
 
 pytestmark = pytest.mark.gpu
 
@@ -47,7 +47,7 @@ class Batch:
         g = torch.Generator().manual_seed(seed)
         return torch.randn((self.n_pad, hq, self.d), generator=g).to(DT[dtype]).cuda()
 
-    def check(self, q, dtype, out, lse, scale=None, precise=None):
+    def check(self, q, dtype, out, lse, scale=None):
         """out and lse of every sequence's tokens against 64 bits, within the derived bounds."""
         scale = 1 / math.sqrt(self.d) if scale is None else scale
         at = 0
@@ -56,7 +56,7 @@ class Batch:
                 continue
             k, v = self.values(b)
             o, z, av, qk = attend(q[at:at + m], k, v, scale)
-            tol, ltol = bounds(o, av, qk, dtype, a, self.d, sixteen=dtype != "f32")
+            tol, ltol = bounds(o, av, qk, dtype, a, self.d, dtype != "f32", offset_terms(self.pair, q[at:at + m], k, v, scale, a))
             got = out[at:at + m].double()
             assert torch.isfinite(got).all(), b
             worst = ((got - o).abs() / tol).max().item()
@@ -301,7 +301,7 @@ def test_attention_value_range(kvq, new, pair, k_mag, v_mag):
     out, lse = cache.attention(q, dev(tab), dev(lens), cu_q=dev([0, new]), max_q=new, scale=scale, return_lse=True)
     ks, vs = (torch.from_numpy(stored(t, x)).cuda() for t, x in zip(pair, (k, v)))
     o, z, av, qk = attend(q, ks, vs, scale)
-    tol, ltol = bounds(o, av, qk, "bf16", 150, 128, True)
+    tol, ltol = bounds(o, av, qk, "bf16", 150, 128, True, offset_terms(pair, q, ks, vs, scale, 150))
     if v_mag < 1:  # 16-bit values below 2^-14 are rounded absolutely, by 2^-25 each, summed with weights of at most 1
         tol = tol + 2.0 ** -24
     assert ((out.double() - o).abs() <= tol).all()
@@ -419,7 +419,8 @@ def test_shared_pages_and_strided_tables(kvq, new):
     for i, (kk, vv) in enumerate(rows):
         ks, vs = torch.from_numpy(stored("q8_0", kk.cpu().numpy())).cuda(), torch.from_numpy(stored("q4_0", vv.cpu().numpy())).cuda()
         o, _, av, qk = attend(q[i * new:(i + 1) * new], ks, vs, 1 / math.sqrt(128))
-        tol, _ = bounds(o, av, qk, "f16", 180, 128, True)
+        tol, _ = bounds(o, av, qk, "f16", 180, 128, True, offset_terms(("q8_0", "q4_0"), q[i * new:(i + 1) * new], ks, vs,
+                                                                                     1 / math.sqrt(128), 180))
         assert ((out[i * new:(i + 1) * new].double() - o).abs() <= tol).all()
 
 
@@ -544,11 +545,11 @@ def test_prompt_then_tokens_as_the_contiguous_cache(kvq, pair):
         ref, ref_lse = flat.decode(r[-1:].contiguous())
         kk, vv = cache.gather(t, dev([at]), at, cu_q=dev([0, at]), max_q=at, dtype=torch.float32)
         o, z, av, qk = attend(r[-1:], kk.double(), vv.double(), 1 / math.sqrt(d))
-        tol, ltol = bounds(o, av, qk, "f32", at, d, False)
+        tol, ltol = bounds(o, av, qk, "f32", at, d, False, offset_terms(pair, r[-1:], kk, vv, 1 / math.sqrt(d), at))
         assert ((out.double() - o).abs() <= tol).all() and ((lse.double() - z).abs() <= ltol).all()
         assert ((ref.double() - out.double()).abs() <= 2 * tol).all()
         chunk = cache.attention(r.bfloat16(), t, dev([at]), **args)
         o, _, av, qk = attend(r.bfloat16(), kk.double(), vv.double(), 1 / math.sqrt(d))
-        tol, _ = bounds(o, av, qk, "bf16", at, d, True)
+        tol, _ = bounds(o, av, qk, "bf16", at, d, True, offset_terms(pair, r, kk, vv, 1 / math.sqrt(d), at))
         assert ((chunk.double() - o).abs() <= tol).all()
     assert cache.read_error() == 0
