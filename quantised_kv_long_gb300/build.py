@@ -17,7 +17,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkvq.so")
 SOURCES = ["kvq_api.cu", "kvq_append.cu", "kvq_decode.cu", "kvq_verify.cu", "kvq_verify_tc.cu", "kvq_decode_ext.cu",
            "kvq_window_dual.cu", "kvq_window_dual1.cu", "kvq_paged_api.cu", "kvq_paged_append.cu", "kvq_paged_attn.cu",
-           "kvq_paged_split_f32.cu", "kvq_paged_split_f16.cu", "kvq_paged_split_bf16.cu"]
+           "kvq_paged_split_f32.cu", "kvq_paged_split_f16.cu", "kvq_paged_split_bf16.cu",
+           "kvq_paged_chunk_f16.cu", "kvq_paged_chunk_bf16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

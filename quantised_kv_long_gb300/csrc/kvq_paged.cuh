@@ -198,6 +198,8 @@ struct PagedAttnParams {
     int Hq, G;
     float scale;
     void *workspace;
+    // sequences with fewer tokens than this belong to the split kernel, the others to the chunk kernel
+    int split_below;
 };
 
 cudaError_t launch_paged_append(int type_k, int type_v, int D, int dtype, const PagedAppendParams &p, cudaStream_t s);
@@ -210,6 +212,56 @@ cudaError_t launch_paged_split_f32(int type_k, int type_v, int D, const PagedAtt
 cudaError_t launch_paged_split_f16(int type_k, int type_v, int D, const PagedAttnParams &p, cudaStream_t s);
 cudaError_t launch_paged_split_bf16(int type_k, int type_v, int D, const PagedAttnParams &p, cudaStream_t s);
 cudaError_t paged_split_workspace(int D, size_t *bytes);
+// many queries per sequence (kvq_paged_chunk.cuh)
+cudaError_t launch_paged_chunk_f16(int type_k, int type_v, int D, const PagedAttnParams &p, cudaStream_t s);
+cudaError_t launch_paged_chunk_bf16(int type_k, int type_v, int D, const PagedAttnParams &p, cudaStream_t s);
+cudaError_t paged_chunk_workspace(int D, size_t *bytes);
+
+// ---- what the attention launches share ----
+constexpr int kPagedMaxDevices = 64;
+// the current device and its SMs (looked up once per device)
+inline cudaError_t paged_device(int *dev, int *sms) {
+    static int cached[kPagedMaxDevices] = {};
+    cudaError_t e = cudaGetDevice(dev);
+    if (e != cudaSuccess) return e;
+    if (*dev < 0 || *dev >= kPagedMaxDevices) return cudaErrorInvalidDevice;
+    if (cached[*dev] == 0) {
+        int n = 0;
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *dev);
+        if (e != cudaSuccess) return e;
+        cached[*dev] = n > 0 ? n : 1;
+    }
+    *sms = cached[*dev];
+    return cudaSuccess;
+}
+// sequences b .. b + most - 1 of a call
+inline PagedAttnParams paged_some(const PagedAttnParams &p, int b, int most) {
+    PagedAttnParams q = p;
+    q.v.n_seqs = p.v.n_seqs - b < most ? p.v.n_seqs - b : most;
+    q.v.lens += b;
+    q.v.table += static_cast<size_t>(b) * p.v.stride;
+    if (p.v.cu_q)
+        q.v.cu_q += b;
+    else
+        q.v.token0 += b;
+    return q;
+}
+// a launch that may start while the previous kernel of its stream finishes (every kernel launched so
+// waits for it before it reads or writes anything)
+template <class... A, class... B>
+cudaError_t launch_dependent(void (*kernel)(A...), dim3 grid, int threads, int smem, cudaStream_t s, B... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 // (K, V) type pairs of the paged cache
 constexpr bool is_paged_pair(int tk, int tv) {

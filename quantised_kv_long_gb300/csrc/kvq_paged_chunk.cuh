@@ -1,0 +1,937 @@
+// kvq_paged_chunk.cuh -- attention of many queries per sequence over the paged cache, on the
+// fifth-generation tensor cores (tcgen05, accumulators in tensor memory).
+//
+// Mathematics: as kvq_paged_split.cuh; token i of a sequence sees positions 0 .. len - n + i.
+//
+// Work.  The n G query rows of a (sequence, KV head) form units of 256 rows (two tiles of 128; one
+// tile for 256-wide heads, whose O fills half of tensor memory).  A unit times a block of 64 keys is
+// a step; all steps of the batch are laid end to end and cut into equal spans, one per CTA (one CTA
+// per SM), so ragged and causal work is even whatever the lengths.  A unit cut by a span boundary
+// leaves pieces (m, l, o) in the workspace, which a second kernel merges.
+//
+// A step, by warps: one thread streams the block's tile records into a ring (one bulk copy per run of
+// tiles in a page); eight warps turn codes into f16 operands K^ (keys x D) and V^ (D x keys) in
+// shared memory, once for all rows of the unit; one thread issues S = Q K^T and O += P V^; four warps
+// per tile hold one row per thread: running maximum, weights, P into tensor memory, and the rescale
+// of O when the maximum moves by more than kChunkDrift.  S of the next block is computed while the
+// softmax of this one runs (S and P have their own columns).
+//
+// Rounding.  Q is f16 after scaling each row by a power of two (exact for f16 and for bf16 in range).
+// K^ and V^ are scale x code rounded once to f16 (2^-11), P is f16 (2^-11); S, O, the maxima and
+// sums are fp32.  The output has 16 bits (2^-11 or 2^-8).  A block with scales that would leave f16
+// is stored times 2^-e, and S or P is multiplied by 2^e, both exact.
+#pragma once
+#include <math_constants.h>
+
+#include "kvq_paged.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr float kChunkLn2 = 0.69314718055994530942f, kChunkLog2e = 1.44269504088896340736f;
+// weights are 2^(s - m + kChunkBias) <= 2^(kChunkBias + kChunkDrift), times 2^e <= 2^9 in f16
+constexpr float kChunkDrift = 4.0f, kChunkBias = 2.0f;
+
+// ---- tcgen05 and tensor memory (inline PTX) ----
+__device__ __forceinline__ void t5_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void t5_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+// shared-memory operand without swizzle: 8-row x 16-byte core matrices, `lbo` bytes apart along K
+// and `sbo` along M or N
+__device__ __forceinline__ uint64_t t5_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (static_cast<uint64_t>((lbo >> 4) & 0x3fffu) << 16) |
+           (static_cast<uint64_t>((sbo >> 4) & 0x3fffu) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+// kind::f16, fp32 accumulator, f16 A and B, both K-major
+__host__ __device__ constexpr uint32_t t5_idesc(int M, int N) {
+    return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ void t5_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void t5_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void t5_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void t5_ld32(uint32_t t, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(t));
+}
+__device__ __forceinline__ void t5_st32(uint32_t t, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+        "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n" ::"r"(t),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+        "r"(r[31]));
+}
+__device__ __forceinline__ void t5_st16(uint32_t t, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n" ::"r"(t),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
+}
+__device__ __forceinline__ void t5_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void t5_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void smem_to_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+__device__ __forceinline__ float chunk_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t perm(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t d;
+    asm("prmt.b32 %0, %1, %2, %3;\n" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+    return d;
+}
+// byte offset of (row, k) in an operand of `kext` elements per row: core matrices of 8 rows x 8 elements
+__device__ __forceinline__ int core_at(int row, int k, int kext) {
+    return (row >> 3) * (kext * 16) + (k >> 3) * 128 + (row & 7) * 16 + (k & 7) * 2;
+}
+
+template <int KT, int VT, int NS>
+struct ChunkCfg {
+    using T = PagedTile<KT, VT, NS>;
+    static constexpr int D = T::D, M = 128, NK = 64, TILES = NK / kTileRows;
+    static constexpr int NT = NS == 1 ? 2 : 1;  // tiles of 128 rows per unit
+    static constexpr int ROWS = NT * M;
+    static constexpr int STAGE = TILES * T::BYTES;
+    static constexpr int KHAT = NK * D * 2, VHAT = NK * D * 2;
+    static constexpr int QSM = NT == 2 ? M * D * 2 : 0;  // Q of tile 1 (tile 0's is in tensor memory)
+    static constexpr int LIMIT = 232448 - 2048;          // of the CTA's shared memory, barriers and statics kept back
+    static constexpr int KB = 2;
+    // two V^ buffers where two raw stages still fit, else one
+    static constexpr int VB = (LIMIT - QSM - KB * KHAT - 2 * VHAT) / STAGE >= 2 ? 2 : 1;
+    static constexpr int OPS = QSM + KB * KHAT + VB * VHAT;
+    static constexpr int STAGES_RAW = (LIMIT - OPS) / STAGE;
+    static constexpr int STAGES = STAGES_RAW > 4 ? 4 : STAGES_RAW;
+    static constexpr int OFF_Q = STAGES * STAGE, OFF_K = OFF_Q + QSM, OFF_V = OFF_K + KB * KHAT;
+    static constexpr int SMEM = OFF_V + VB * VHAT;
+    // tensor memory columns: O of each tile, S of each, P of each, Q of tile 0
+    static constexpr int T_O = 0, T_S = NT * D, T_P = T_S + NT * NK, T_Q = T_P + NT * NK / 2;
+    static_assert(T_Q + D / 2 <= 512, "tensor memory");
+    static_assert(STAGES >= 2 && SMEM <= LIMIT, "shared memory");
+    static constexpr int SOFT0 = 4, CONV0 = SOFT0 + 4 * NT, CONV_WARPS = 8;  // first softmax / converter warp
+    static constexpr int WARPS = CONV0 + CONV_WARPS;
+    static constexpr int THREADS = WARPS * 32;
+};
+
+// ---- workspace: [per CTA: the unit it starts in][pieces: m, l][pieces: o] ----
+struct ChunkWork {
+    int32_t *first;  // [CTAs][8]: sequence, head, unit, the unit's first step, its steps, span
+    float *ml;       // [2 CTAs][ROWS][2]
+    float *o;        // [2 CTAs][ROWS][D]
+};
+inline ChunkWork chunk_work(void *ws, int ctas, int rows, int D, size_t *bytes) {
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    const size_t head = (static_cast<size_t>(ctas) * 32 + 255) / 256 * 256, ml = static_cast<size_t>(2) * ctas * rows * 8;
+    if (bytes) *bytes = head + ml + static_cast<size_t>(2) * ctas * rows * D * 4;
+    return ChunkWork{reinterpret_cast<int32_t *>(w), reinterpret_cast<float *>(w + head), reinterpret_cast<float *>(w + head + ml)};
+}
+
+constexpr int kChunkMaxSeqs = 256;  // sequences of one launch (their prefix sums sit in shared memory)
+
+// Units of a sequence and their steps.  A unit has at least one step, so that rows which attend to
+// nothing are written too.
+struct ChunkSeq {
+    int first, n, len, units;  // units per KV head
+};
+template <int ROWS>
+__device__ __forceinline__ ChunkSeq chunk_seq(const PagedView &v, int G, int min_q, int b) {
+    const PagedSeq s = paged_seq(v, b);
+    ChunkSeq c;
+    c.first = s.first;
+    c.n = s.n >= min_q ? s.n : 0;  // shorter ones belong to the split kernel
+    c.len = s.len;
+    c.units = static_cast<int>((static_cast<long long>(c.n) * G + ROWS - 1) / ROWS);
+    return c;
+}
+template <int ROWS, int NK>
+__device__ __forceinline__ int chunk_steps(const ChunkSeq &s, int G, int u) {
+    const long long last_row = min(static_cast<long long>(s.n) * G, (static_cast<long long>(u) + 1) * ROWS) - 1;
+    const int last = s.len - s.n + static_cast<int>(last_row / G);  // last position any row sees
+    return max(1, (last + NK) / NK);
+}
+
+// A walk over the units of a span: unit u of head h of sequence b, its steps, and the range of them
+// that belongs to this CTA.
+struct ChunkWalk {
+    ChunkSeq s;
+    int b, h, u, steps;
+};
+
+template <int KT, int VT, int NS, int DT>
+__global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
+    paged_chunk_kernel(const PagedAttnParams p, const ChunkWork work) {
+    using C = ChunkCfg<KT, VT, NS>;
+    using T = typename C::T;
+    using X = typename Act<DT>::type;
+    constexpr int D = C::D, NK = C::NK, NT = C::NT, ROWS = C::ROWS;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t raw_full[4], raw_empty[4], k_ready[2], k_free[2], v_ready[2], v_free[2];
+    __shared__ __align__(8) uint64_t s_ready[2], s_free[2], p_ready[2], pv_done[2], q_ready[2], drain;
+    __shared__ int s_pre[kChunkMaxSeqs + 1];
+    __shared__ int s_start[4];                       // sequence, head, unit, step of this CTA's first step
+    __shared__ int s_ok[8], s_exp[8][2];             // per block: copied tiles; exponents of K^ and V^
+    __shared__ uint32_t s_tmem;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const PagedView &v = p.v;
+    const int G = p.G;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(raw_full + i, 1);
+            mbar_init(raw_empty + i, C::CONV_WARPS);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(k_ready + i, C::CONV_WARPS);
+            mbar_init(k_free + i, 1);
+            mbar_init(v_ready + i, C::CONV_WARPS);
+            mbar_init(v_free + i, 1);
+            mbar_init(s_ready + i, 1);
+            mbar_init(s_free + i, 4);
+            mbar_init(p_ready + i, 4);
+            mbar_init(pv_done + i, 1);
+            mbar_init(q_ready + i, 4);
+        }
+        mbar_init(&drain, 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&s_tmem)), "r"(512));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+    }
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+
+    // ---- steps before each sequence, and where this CTA starts ----
+    for (int b = warp; b < v.n_seqs; b += C::WARPS) {
+        const ChunkSeq s = chunk_seq<ROWS>(v, G, p.split_below, b);
+        int sum = 0;
+        for (int u = lane; u < s.units; u += 32) sum += chunk_steps<ROWS, NK>(s, G, u);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) s_pre[b + 1] = sum * v.Hkv;
+        if (blockIdx.x == 0 && lane == 0 && !paged_seq(v, b).ok) paged_error(v);
+    }
+    t5_fence_before();
+    __syncthreads();
+    t5_fence_after();
+    if (warp == 0) {
+        int base = 0;
+        if (lane == 0) s_pre[0] = 0;
+        for (int b0 = 0; b0 < v.n_seqs; b0 += 32) {
+            int x = b0 + lane < v.n_seqs ? s_pre[b0 + lane + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (b0 + lane < v.n_seqs) s_pre[b0 + lane + 1] = base + x;
+            base += __shfl_sync(0xffffffffu, x, 31);
+        }
+    }
+    __syncthreads();
+    const int total = s_pre[v.n_seqs];
+    // at least kMinSpan steps per CTA: shorter spans cost more in pieces than they gain
+    constexpr int kMinSpan = 4;
+    const int span = max(kMinSpan, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+    const long long x0l = static_cast<long long>(blockIdx.x) * span;
+    const int x0 = x0l < total ? static_cast<int>(x0l) : total, x1 = min(total, x0 + span);
+    const int NX = x1 - x0;  // steps of this CTA
+    if (NX > 0 && warp == 0) {
+        int lo = 0, hi = v.n_seqs;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_pre[mid] <= x0)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const ChunkSeq s = chunk_seq<ROWS>(v, G, p.split_below, lo);
+        const int per_head = (s_pre[lo + 1] - s_pre[lo]) / v.Hkv;
+        int r = x0 - s_pre[lo];
+        const int h = r / per_head;
+        r -= h * per_head;
+        // the unit: 32 at a time
+        for (int u0 = 0; u0 < s.units; u0 += 32) {
+            const int own = u0 + lane < s.units ? chunk_steps<ROWS, NK>(s, G, u0 + lane) : 0;
+            int inc = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, r < inc);
+            if (hit) {
+                const int w = __ffs(hit) - 1;
+                const int before = __shfl_sync(0xffffffffu, inc - own, w);
+                if (lane == 0) {
+                    s_start[0] = lo;
+                    s_start[1] = h;
+                    s_start[2] = u0 + w;
+                    s_start[3] = r - before;
+                }
+                break;
+            }
+            r -= __shfl_sync(0xffffffffu, inc, 31);
+        }
+    }
+    __syncthreads();
+    const uint32_t tm = s_tmem;
+
+    // every role walks the same segments: [c0, c1) are the steps of unit (b, h, u) in this CTA
+    auto begin = [&]() {
+        ChunkWalk w;
+        w.b = s_start[0];
+        w.h = s_start[1];
+        w.u = s_start[2];
+        w.s = chunk_seq<ROWS>(v, G, p.split_below, w.b);
+        w.steps = chunk_steps<ROWS, NK>(w.s, G, w.u);
+        return w;
+    };
+    auto advance = [&](ChunkWalk &w) {
+        if (++w.u == w.s.units) {
+            w.u = 0;
+            if (++w.h == v.Hkv) {
+                w.h = 0;
+                ++w.b;
+                while (s_pre[w.b + 1] == s_pre[w.b]) ++w.b;
+                w.s = chunk_seq<ROWS>(v, G, p.split_below, w.b);
+            }
+        }
+        w.steps = chunk_steps<ROWS, NK>(w.s, G, w.u);
+    };
+    // rows of tile t in a unit
+    auto tile_rows = [&](const ChunkWalk &w, int t) {
+        const long long left = static_cast<long long>(w.s.n) * G - static_cast<long long>(w.u) * ROWS - t * C::M;
+        return static_cast<int>(left < 0 ? 0 : (left > C::M ? C::M : left));
+    };
+
+    if (NX > 0) {
+        if (warp == 0) {
+            // ---------------- copies ----------------
+            if (lane == 0) {
+                ChunkWalk w = begin();
+                int t = s_start[3], issued = 0;
+                bool ok = true;
+                const size_t page_bytes = static_cast<size_t>(v.page_tiles) * T::BYTES;
+                for (int x = 0; x < NX; ++x) {
+                    const int st = x % C::STAGES, use = x / C::STAGES;
+                    if (use > 0 && !mbar_wait(raw_empty + st, (use - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const int tile0 = t * C::TILES, tiles = (w.s.len + kTileRows - 1) / kTileRows;
+                    const int32_t *row = v.table + static_cast<size_t>(w.b) * v.stride;
+                    const uint8_t *src[C::TILES];
+                    int got = 0;
+                    int e = tile0 / v.page_tiles, q = tile0 - e * v.page_tiles;
+#pragma unroll
+                    for (int i = 0; i < C::TILES; ++i) {
+                        src[i] = nullptr;
+                        if (tile0 + i < tiles) {
+                            const int page = __ldg(row + e);
+                            if (page >= 0 && page < v.n_pages) {
+                                src[i] = v.pool + (static_cast<size_t>(page) * v.Hkv + w.h) * page_bytes + static_cast<size_t>(q) * T::BYTES;
+                                got |= 1 << i;
+                            } else {
+                                paged_error(v);
+                            }
+                        }
+                        if (++q == v.page_tiles) q = 0, ++e;
+                    }
+                    s_ok[x & 7] = got;
+                    mbar_arrive_expect_tx(raw_full + st, static_cast<uint32_t>(__popc(got) * T::BYTES));
+                    uint8_t *dst = smem + st * C::STAGE;
+#pragma unroll
+                    for (int i = 0; i < C::TILES; ++i)
+                        if (src[i]) bulk_g2s(dst + i * T::BYTES, src[i], T::BYTES, raw_full + st);
+                    issued = x + 1;
+                    if (++t == w.steps && x + 1 < NX) {
+                        advance(w);
+                        t = 0;
+                    }
+                }
+                if (!ok) atomicOr(v.err, KVQ_DEVERR_TIMEOUT);
+                for (int i = 0; i < C::STAGES; ++i)  // every copy lands before the memory is freed
+                    if (i < issued) {
+                        const int lastx = (issued - 1 - i) / C::STAGES;  // last use of stage i
+                        (void)mbar_wait(raw_full + i, lastx & 1);
+                    }
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ---------------- MMA issue ----------------
+            if (lane == 0) {
+                constexpr uint32_t ID_S = t5_idesc(C::M, NK), ID_O = t5_idesc(C::M, D);
+                const uint64_t qd = t5_desc(smem_u32(smem + C::OFF_Q), 128, D * 16);
+                uint64_t kd[C::KB], vd[C::VB];
+                for (int i = 0; i < C::KB; ++i) kd[i] = t5_desc(smem_u32(smem + C::OFF_K + i * C::KHAT), 128, D * 16);
+                for (int i = 0; i < C::VB; ++i) vd[i] = t5_desc(smem_u32(smem + C::OFF_V + i * C::VHAT), 128, NK * 16);
+                auto qk = [&](int t, int x) {  // S_t = Q_t K^(x)^T
+                    const uint64_t b = kd[x % C::KB];
+                    const uint32_t d = tm + C::T_S + t * NK;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        if (t == 0)
+                            t5_mma_ts(d, tm + C::T_Q + 8 * k, b + 16 * k, ID_S, k > 0);
+                        else
+                            t5_mma_ss(d, qd + 16 * k, b + 16 * k, ID_S, k > 0);
+                    }
+                    t5_commit(s_ready + t);
+                };
+                auto pv = [&](int t, int x, bool start) {  // O_t += P_t V^(x)
+                    const uint64_t b = vd[x % C::VB];
+#pragma unroll
+                    for (int k = 0; k < NK / 16; ++k)
+                        t5_mma_ts(tm + C::T_O + t * D, tm + C::T_P + t * (NK / 2) + 8 * k, b + 16 * k, ID_O, !start || k > 0);
+                    t5_commit(pv_done + t);
+                };
+                ChunkWalk w = begin();
+                int c0 = s_start[3], x = 0;
+                int done[2] = {0, 0}, segs[2] = {0, 0};  // steps and segments of each tile so far (phases of its barriers)
+                bool ok = true;
+                while (x < NX && ok) {
+                    const int n = min(w.steps - c0, NX - x);  // steps of this segment
+                    const int nt = NT == 2 && tile_rows(w, 1) > 0 ? 2 : 1;
+                    ok = mbar_wait(k_ready + x % C::KB, (x / C::KB) & 1);
+                    for (int t = 0; t < nt && ok; ++t) {
+                        // a tile's queries are staged once its last segment's O has been read
+                        ok = mbar_wait(q_ready + t, segs[t]++ & 1);
+                        t5_fence_after();
+                        if (ok) qk(t, x);
+                    }
+                    if (ok) t5_commit(k_free + x % C::KB);
+                    for (int c = 0; c < n && ok; ++c) {
+                        const bool more = c + 1 < n;
+                        if (more) ok = mbar_wait(k_ready + (x + 1) % C::KB, ((x + 1) / C::KB) & 1);
+                        for (int t = 0; t < nt && ok; ++t) {
+                            if (more) {
+                                ok = mbar_wait(s_free + t, done[t] & 1);
+                                t5_fence_after();
+                                if (!ok) break;
+                                qk(t, x + 1);
+                                if (t == nt - 1) t5_commit(k_free + (x + 1) % C::KB);
+                            }
+                            if (t == 0) ok = mbar_wait(v_ready + x % C::VB, (x / C::VB) & 1);
+                            ok = ok && mbar_wait(p_ready + t, done[t] & 1);
+                            t5_fence_after();
+                            if (!ok) break;
+                            pv(t, x, c == 0);
+                            if (t == nt - 1) t5_commit(v_free + x % C::VB);
+                            ++done[t];
+                        }
+                        ++x;
+                    }
+                    if (x < NX && ok) advance(w);
+                    c0 = 0;
+                }
+                if (!ok) atomicOr(v.err, KVQ_DEVERR_TIMEOUT);
+                t5_commit(&drain);  // every MMA has completed before tensor memory is freed
+                (void)mbar_wait(&drain, 0);
+            }
+            __syncwarp();
+        } else if (warp >= C::CONV0) {
+            // ---------------- converters: codes -> K^, V^ ----------------
+            const int cw = warp - C::CONV0;
+            constexpr int NCW = C::CONV_WARPS;
+            const uint32_t magic = 0x64006400u;  // f16 1024 | bits = 1024 + bits
+            const __half2 k1024 = __float2half2_rn(1024.0f), k1032 = __float2half2_rn(1032.0f);
+            const __half2 k16th = __float2half2_rn(0.0625f), km72 = __float2half2_rn(-72.0f);
+            auto q8pair = [&](uint32_t word, uint32_t sel_mag, uint32_t sel_sign) {  // two sign-magnitude bytes
+                const uint32_t m = (perm(word, 0u, sel_mag) & 0x007f007fu) | magic;
+                const uint32_t sg = perm(word, 0u, sel_sign) & 0x80008000u;
+                return u32_as_h2(h2_as_u32(__hsub2(u32_as_h2(m), k1024)) | sg);
+            };
+            auto q4lo = [&](uint32_t x) { return __hsub2(u32_as_h2((x & 0x000f000fu) | magic), k1032); };
+            auto q4hi = [&](uint32_t x) { return __hfma2(u32_as_h2((x & 0x00f000f0u) | magic), k16th, km72); };
+            auto both = [](uint32_t w, int upper) { return perm(w, 0u, upper ? 0x3232u : 0x1010u); };  // one half twice
+            // rows of tile i of block x in use
+            auto rows_of = [&](int len, int t, int got, int i) {
+                return ((got >> i) & 1) ? max(0, min(kTileRows, len - (t * C::TILES + i) * kTileRows)) : 0;
+            };
+            // exponent e >= 0 with the block's largest |scale| cmax 2^-e at most 2^14, over the rows in use
+            auto block_exp = [&](const uint8_t *st, int off, float cmax, int len, int t, int got) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int k = 0; k < NS; ++k) {
+                    const int gi = k * 32 + lane, i = gi / (8 * NS), in = gi % (8 * NS);  // tile, 16-byte group of its scales
+                    uint4 w = *reinterpret_cast<const uint4 *>(st + i * T::BYTES + off + in * 16);
+                    const int use = rows_of(len, t, got, i), ka = 2 * ((in & 7) >> 1);
+                    if (use < kTileRows) {
+                        auto cut = [&](uint32_t x, int r) { return r >= use ? 0u : (r + 1 >= use ? (x & 0xffffu) : x); };
+                        w = make_uint4(cut(w.x, ka), cut(w.y, ka + 8), cut(w.z, ka), cut(w.w, ka + 8));
+                    }
+                    const __half2 a = __hmax2(__habs2(u32_as_h2(w.x)), __habs2(u32_as_h2(w.y)));
+                    const __half2 b = __hmax2(__habs2(u32_as_h2(w.z)), __habs2(u32_as_h2(w.w)));
+                    m = h2_as_u32(__hmax2(u32_as_h2(m), __hmax2(a, b)));
+                }
+                float2 f = __half22float2(u32_as_h2(m));
+                float top = fmaxf(f.x, f.y) * cmax;
+                if (!__any_sync(0xffffffffu, top > 16384.f)) return 0;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                return min(9, max(0, ilogbf(top) - 13));
+            };
+            auto pow2 = [](int e) { return __int_as_float((127 + e) << 23); };
+
+            ChunkWalk w = begin();
+            int t = s_start[3];
+            bool ok = true;
+            for (int x = 0; x < NX && ok; ++x) {
+                const int sg = x % C::STAGES;
+                const uint8_t *st = smem + sg * C::STAGE;
+                ok = mbar_wait(raw_full + sg, (x / C::STAGES) & 1);
+                if (x >= C::KB) ok = mbar_wait(k_free + x % C::KB, (x / C::KB - 1) & 1) && ok;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const int got = s_ok[x & 7], len = w.s.len;
+                int ek = 0, ev = 0;
+                if constexpr (KT != KVQ_F16) ek = block_exp(st, T::OFF_KS, KT == KVQ_Q8_0 ? 127.f : 8.f, len, t, got);
+                if constexpr (VT != KVQ_F16) ev = block_exp(st, T::OFF_VS, VT == KVQ_Q8_0 ? 127.f : 8.f, len, t, got);
+                if (cw == 0 && lane == 0) {
+                    s_exp[x & 7][0] = ek;
+                    s_exp[x & 7][1] = ev;
+                }
+                // ---- K^ ----
+                {
+                    uint8_t *kh = smem + C::OFF_K + (x % C::KB) * C::KHAT;
+                    const __half2 fk = __float2half2_rn(pow2(-ek));
+                    const int n = lane >> 2, jd = lane & 3;  // key n (and n + 8) of the tile, 4-value group jd
+                    auto put = [&](int key, int dim, __half2 c01, __half2 c23, __half2 d2) {
+                        *reinterpret_cast<uint2 *>(kh + core_at(key, dim, D)) = make_uint2(h2_as_u32(__hmul2(c01, d2)), h2_as_u32(__hmul2(c23, d2)));
+                    };
+                    if constexpr (KT == KVQ_Q8_0) {
+#pragma unroll
+                        for (int wu = cw; wu < C::TILES * NS * 4; wu += NCW) {
+                            const int ts = wu >> 2, b = wu & 3, i = ts / NS, sl = ts % NS;
+                            const uint8_t *tile = st + i * T::BYTES;
+                            const uint4 c = *reinterpret_cast<const uint4 *>(tile + sl * 2048 + (b * 32 + lane) * 16);
+                            const uint2 sc = *reinterpret_cast<const uint2 *>(tile + T::OFF_KS + sl * kScaleTile + (n >> 1) * 32 + b * 8);
+                            const int k0 = i * kTileRows + n, dim = sl * kSlice + 32 * b + 4 * jd;
+                            const __half2 da = __hmul2(u32_as_h2(both(sc.x, n & 1)), fk), db = __hmul2(u32_as_h2(both(sc.y, n & 1)), fk);
+                            put(k0, dim, q8pair(c.x, 0x4140u, 0x1404u), q8pair(c.x, 0x4342u, 0x3424u), da);
+                            put(k0, dim + 16, q8pair(c.y, 0x4140u, 0x1404u), q8pair(c.y, 0x4342u, 0x3424u), da);
+                            put(k0 + 8, dim, q8pair(c.z, 0x4140u, 0x1404u), q8pair(c.z, 0x4342u, 0x3424u), db);
+                            put(k0 + 8, dim + 16, q8pair(c.w, 0x4140u, 0x1404u), q8pair(c.w, 0x4342u, 0x3424u), db);
+                        }
+                    } else if constexpr (KT == KVQ_Q4_0) {
+#pragma unroll
+                        for (int wu = cw; wu < C::TILES * NS * 2; wu += NCW) {
+                            const int ts = wu >> 1, b2 = wu & 1, i = ts / NS, sl = ts % NS;
+                            const uint8_t *tile = st + i * T::BYTES;
+                            const uint4 c = *reinterpret_cast<const uint4 *>(tile + sl * 1024 + (b2 * 32 + lane) * 16);
+                            const uint4 sc = *reinterpret_cast<const uint4 *>(tile + T::OFF_KS + sl * kScaleTile + (n >> 1) * 32 + b2 * 16);
+                            const uint32_t cs[4] = {c.x, c.y, c.z, c.w}, ss[4] = {sc.x, sc.y, sc.z, sc.w};
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {  // block 2 b2 + q / 2, key n + 8 (q % 2)
+                                const int key = i * kTileRows + n + 8 * (q & 1), dim = sl * kSlice + 64 * b2 + 32 * (q >> 1) + 4 * jd;
+                                const __half2 d2 = __hmul2(u32_as_h2(both(ss[q], n & 1)), fk);
+                                const uint32_t w01 = perm(cs[q], 0u, 0x4140u), w23 = perm(cs[q], 0u, 0x4342u);
+                                put(key, dim, q4lo(w01), q4lo(w23), d2);
+                                put(key, dim + 16, q4hi(w01), q4hi(w23), d2);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int wu = cw; wu < C::TILES * NS * 8; wu += NCW) {
+                            const int ts = wu >> 3, ch = wu & 7, i = ts / NS, sl = ts % NS;
+                            const uint4 c = *reinterpret_cast<const uint4 *>(st + i * T::BYTES + sl * 4096 + (ch * 32 + lane) * 16);
+                            const int key = i * kTileRows + n + 8 * (ch & 1), dim = sl * kSlice + 32 * (ch >> 1) + 4 * jd;
+                            *reinterpret_cast<uint2 *>(kh + core_at(key, dim, D)) = make_uint2(perm(c.x, c.y, 0x5410u), perm(c.x, c.y, 0x7632u));
+                            *reinterpret_cast<uint2 *>(kh + core_at(key, dim + 16, D)) = make_uint2(perm(c.z, c.w, 0x5410u), perm(c.z, c.w, 0x7632u));
+                        }
+                    }
+                    smem_to_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(k_ready + x % C::KB);
+                }
+                // ---- V^: rows past the sequence's end may hold any bits and become 0 ----
+                if (x >= C::VB) ok = __all_sync(0xffffffffu, mbar_wait(v_free + x % C::VB, (x / C::VB - 1) & 1));
+                if (!ok) break;
+                {
+                    uint8_t *vh = smem + C::OFF_V + (x % C::VB) * C::VHAT;
+                    const __half2 fv = __float2half2_rn(pow2(-ev));
+                    const int np = lane >> 2, j = lane & 3;
+                    auto put = [&](int dim, int k0, __half2 ca, __half2 cb, __half2 da, __half2 db) {
+                        uint8_t *at = vh + core_at(dim, k0, NK);  // keys k0, k0 + 1 and k0 + 8, k0 + 9
+                        *reinterpret_cast<uint32_t *>(at) = h2_as_u32(__hmul2(ca, da));
+                        *reinterpret_cast<uint32_t *>(at + 128) = h2_as_u32(__hmul2(cb, db));
+                    };
+                    auto cut = [&](uint32_t s2, int r, int use) { return r >= use ? 0u : (r + 1 >= use ? (s2 & 0xffffu) : s2); };
+                    if constexpr (VT == KVQ_Q8_0) {
+#pragma unroll
+                        for (int wu = cw; wu < C::TILES * NS * 4; wu += NCW) {
+                            const int ts = wu >> 2, b = wu & 3, i = ts / NS, sl = ts % NS;
+                            const uint8_t *tile = st + i * T::BYTES;
+                            const uint4 c = *reinterpret_cast<const uint4 *>(tile + T::OFF_V + sl * 2048 + (b * 32 + lane) * 16);
+                            const uint2 sc = *reinterpret_cast<const uint2 *>(tile + T::OFF_VS + sl * kScaleTile + j * 32 + b * 8);
+                            const int use = rows_of(len, t, got, i);
+                            const __half2 da = __hmul2(u32_as_h2(cut(sc.x, 2 * j, use)), fv), db = __hmul2(u32_as_h2(cut(sc.y, 2 * j + 8, use)), fv);
+                            const uint32_t cs[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                put(sl * kSlice + 32 * b + 16 * (q >> 1) + 2 * np + (q & 1), i * kTileRows + 2 * j, q8pair(cs[q], 0x4240u, 0x2404u),
+                                    q8pair(cs[q], 0x4341u, 0x3414u), da, db);
+                        }
+                    } else if constexpr (VT == KVQ_Q4_0) {
+#pragma unroll
+                        for (int wu = cw; wu < C::TILES * NS * 2; wu += NCW) {
+                            const int ts = wu >> 1, b2 = wu & 1, i = ts / NS, sl = ts % NS;
+                            const uint8_t *tile = st + i * T::BYTES;
+                            const uint4 c = *reinterpret_cast<const uint4 *>(tile + T::OFF_V + sl * 1024 + (b2 * 32 + lane) * 16);
+                            const uint4 sc = *reinterpret_cast<const uint4 *>(tile + T::OFF_VS + sl * kScaleTile + j * 32 + b2 * 16);
+                            const int use = rows_of(len, t, got, i), k0 = i * kTileRows + 2 * j;
+                            const __half2 d[4] = {__hmul2(u32_as_h2(cut(sc.x, 2 * j, use)), fv), __hmul2(u32_as_h2(cut(sc.y, 2 * j + 8, use)), fv),
+                                                  __hmul2(u32_as_h2(cut(sc.z, 2 * j, use)), fv), __hmul2(u32_as_h2(cut(sc.w, 2 * j + 8, use)), fv)};
+                            const uint32_t cs[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {  // block 2 b2 + q / 2, value 2 np + q % 2 (and + 16)
+                                const int dim = sl * kSlice + 64 * b2 + 32 * (q >> 1) + 2 * np + (q & 1);
+                                const uint32_t wa = perm(cs[q], 0u, 0x4240u), wb = perm(cs[q], 0u, 0x4341u);
+                                put(dim, k0, q4lo(wa), q4lo(wb), d[2 * (q >> 1)], d[2 * (q >> 1) + 1]);
+                                put(dim + 16, k0, q4hi(wa), q4hi(wb), d[2 * (q >> 1)], d[2 * (q >> 1) + 1]);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int wu = cw; wu < C::TILES * NS * 8; wu += NCW) {
+                            const int ts = wu >> 3, ch = wu & 7, i = ts / NS, sl = ts % NS;
+                            const uint4 c = *reinterpret_cast<const uint4 *>(st + i * T::BYTES + T::OFF_V + sl * 4096 + (ch * 32 + lane) * 16);
+                            const int use = rows_of(len, t, got, i), dim = sl * kSlice + 32 * (ch >> 1) + 16 * (ch & 1) + 2 * np;
+                            uint8_t *at = vh + core_at(dim, i * kTileRows + 2 * j, NK);
+                            *reinterpret_cast<uint32_t *>(at) = cut(c.x, 2 * j, use);
+                            *reinterpret_cast<uint32_t *>(at + 128) = cut(c.y, 2 * j + 8, use);
+                            *reinterpret_cast<uint32_t *>(at + 16) = cut(c.z, 2 * j, use);  // dim is even: dim + 1 is the next row
+                            *reinterpret_cast<uint32_t *>(at + 144) = cut(c.w, 2 * j + 8, use);
+                        }
+                    }
+                    smem_to_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(v_ready + x % C::VB);
+                        mbar_arrive(raw_empty + sg);  // the stage has been read
+                    }
+                }
+                if (++t == w.steps && x + 1 < NX) {
+                    advance(w);
+                    t = 0;
+                }
+            }
+            if (!ok && lane == 0) atomicOr(v.err, KVQ_DEVERR_TIMEOUT);
+        } else if (warp >= C::SOFT0 && warp < C::CONV0) {
+            // ---------------- one query row per thread ----------------
+            const int tile = (warp - C::SOFT0) >> 2, quarter = warp & 3;
+            const int r = 32 * quarter + lane;  // row of the tile = lane of tensor memory
+            const uint32_t trow = tm + (static_cast<uint32_t>(32 * quarter) << 16);
+            const uint32_t tS = trow + C::T_S + tile * NK, tP = trow + C::T_P + tile * (NK / 2), tO = trow + C::T_O + tile * D;
+            ChunkWalk w = begin();
+            int c0 = s_start[3], x = 0, done = 0;
+            bool ok = true;
+            while (x < NX && ok) {
+                const int n = min(w.steps - c0, NX - x);
+                const int rows = tile_rows(w, tile);
+                const bool live = rows > 0;
+                const long long rr = static_cast<long long>(w.u) * ROWS + tile * C::M + r;  // row of the (sequence, head)
+                const bool rv = r < rows;
+                const int i = rv ? static_cast<int>(rr / G) : 0;
+                const size_t orow = (static_cast<size_t>(w.s.first) + i) * p.Hq + static_cast<size_t>(w.h) * G + (rv ? rr % G : 0);
+                const int lim = w.s.len - w.s.n + i;  // last position of the row
+                // ---- the row's query, scaled to a largest value of 2^10 .. 2^11 ----
+                const X *src = static_cast<const X *>(p.q) + (static_cast<size_t>(w.s.first) + i) * p.q_stride +
+                               (static_cast<size_t>(w.h) * G + (rv ? rr % G : 0)) * D;
+                float rs = 0.f;
+                if (live) {
+                    float top = 0.f;
+                    if (rv)
+                        for (int d = 0; d < D; d += 4) {
+                            const float4 q4 = Act<DT>::load4(src + d);
+                            top = fmaxf(top, fmaxf(fmaxf(fabsf(q4.x), fabsf(q4.y)), fmaxf(fabsf(q4.z), fabsf(q4.w))));
+                        }
+                    const int ex = static_cast<int>(__float_as_uint(top) >> 23);
+                    int k = top == 0.f || ex == 255 ? 0 : 10 - (ex - 127);
+                    k = max(-120, min(120, k));
+                    float up = __int_as_float((127 + k) << 23);
+                    rs = fabsf(p.scale) * kChunkLog2e * __int_as_float((127 - k) << 23);
+                    if (p.scale < 0.f) up = -up;  // rs >= 0: the largest score is the largest product
+#pragma unroll 1
+                    for (int d0 = 0; d0 < D; d0 += 32) {
+                        uint32_t h[16];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float4 q4 = rv ? Act<DT>::load4(src + d0 + 4 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
+                            h[2 * e] = h2_as_u32(__floats2half2_rn(q4.x * up, q4.y * up));
+                            h[2 * e + 1] = h2_as_u32(__floats2half2_rn(q4.z * up, q4.w * up));
+                        }
+                        if (tile == 0) {
+                            t5_st16(trow + C::T_Q + d0 / 2, h);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                *reinterpret_cast<uint4 *>(smem + C::OFF_Q + core_at(r, d0 + 8 * e, D)) =
+                                    make_uint4(h[4 * e], h[4 * e + 1], h[4 * e + 2], h[4 * e + 3]);
+                        }
+                    }
+                    if (tile == 0)
+                        t5_wait_st();
+                    else
+                        smem_to_async();
+                }
+                t5_fence_before();
+                __syncwarp();
+                if (live && lane == 0) mbar_arrive(q_ready + tile);
+                float m_run = -CUDART_INF_F, l = 0.f;
+                if (!live) {
+                    x += n;
+                } else {
+                    for (int c = 0; c < n && ok; ++c, ++x, ++done) {
+                        ok = __all_sync(0xffffffffu, mbar_wait(s_ready + tile, done & 1));
+                        if (!ok) break;
+                        t5_fence_after();
+                        uint32_t su[NK];
+                        t5_ld32(tS, su);
+                        t5_ld32(tS + 32, su + 32);
+                        const int got = s_ok[x & 7], ek = s_exp[x & 7][0], ev = s_exp[x & 7][1];
+                        t5_wait_ld();
+                        t5_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(s_free + tile);
+                        float s[NK];
+#pragma unroll
+                        for (int k = 0; k < NK; ++k) s[k] = __uint_as_float(su[k]);
+                        // never 0, so that a masked score stays -inf
+                        const float f = fmaxf(rs * __int_as_float((127 + ek) << 23), 1e-36f);
+                        // keys behind the row's position (and so past the end) and those in no page
+                        const int key0 = (c0 + c) * NK;
+                        if (__any_sync(0xffffffffu, rv && key0 + NK - 1 > lim) || got != (1 << C::TILES) - 1) {
+#pragma unroll
+                            for (int k = 0; k < NK; ++k)
+                                if (key0 + k > lim || !((got >> (k / kTileRows)) & 1)) s[k] = -CUDART_INF_F;
+                        }
+                        float mx = s[0];
+#pragma unroll
+                        for (int k = 1; k < NK; ++k) mx = fmaxf(mx, s[k]);
+                        mx *= f;
+                        const bool need = mx > m_run + kChunkDrift;
+                        float alpha = 1.f;
+                        if (need) {
+                            alpha = m_run == -CUDART_INF_F ? 0.f : chunk_ex2(m_run - mx);
+                            m_run = mx;
+                            l *= alpha;
+                        }
+                        const float base = (m_run == -CUDART_INF_F ? 0.f : m_run) - kChunkBias;
+                        uint32_t pw[NK / 2];
+                        const float fe = __int_as_float((127 + ev) << 23);
+#pragma unroll
+                        for (int k = 0; k < NK / 2; ++k) {
+                            const float a = chunk_ex2(fmaf(s[2 * k], f, -base)), b = chunk_ex2(fmaf(s[2 * k + 1], f, -base));
+                            l += a + b;
+                            pw[k] = h2_as_u32(__floats2half2_rn(a * fe, b * fe));
+                        }
+                        // P and O are free once the previous block's P V^ is done
+                        if (c > 0) ok = __all_sync(0xffffffffu, mbar_wait(pv_done + tile, (done - 1) & 1));
+                        if (!ok) break;
+                        t5_fence_after();
+                        if (c > 0 && __any_sync(0xffffffffu, need)) {
+#pragma unroll 1
+                            for (int d0 = 0; d0 < D; d0 += 32) {
+                                uint32_t o[32];
+                                t5_ld32(tO + d0, o);
+                                t5_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                t5_st32(tO + d0, o);
+                            }
+                        }
+                        t5_st32(tP, pw);
+                        t5_wait_st();
+                        t5_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(p_ready + tile);
+                    }
+                    if (!ok) break;
+                    ok = __all_sync(0xffffffffu, mbar_wait(pv_done + tile, (done - 1) & 1));
+                    if (!ok) break;
+                    t5_fence_after();
+                    const bool whole = c0 == 0 && n == w.steps;
+                    if (whole) {
+                        const float inv = l > 0.f ? 1.f / l : 0.f;
+                        X *dst = static_cast<X *>(p.out) + orow * D;
+#pragma unroll 1
+                        for (int d0 = 0; d0 < D; d0 += 32) {
+                            uint32_t o[32];
+                            t5_ld32(tO + d0, o);
+                            t5_wait_ld();
+                            if (rv)
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    Act<DT>::store4(dst + d0 + 4 * e, make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                                                                  __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv));
+                        }
+                        if (rv && p.lse) p.lse[orow] = l > 0.f ? (m_run - kChunkBias + __log2f(l)) * kChunkLn2 : -CUDART_INF_F;
+                    } else {
+                        // the first segment of the CTA, or its last
+                        const size_t piece = (static_cast<size_t>(2) * blockIdx.x + (x - n > 0 ? 1 : 0)) * ROWS + tile * C::M + r;
+                        float *dst = work.o + piece * D;
+#pragma unroll 1
+                        for (int d0 = 0; d0 < D; d0 += 32) {
+                            uint32_t o[32];
+                            t5_ld32(tO + d0, o);
+                            t5_wait_ld();
+                            if (rv)
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    *reinterpret_cast<uint4 *>(dst + d0 + 4 * e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        }
+                        work.ml[2 * piece] = m_run == -CUDART_INF_F ? -CUDART_INF_F : m_run - kChunkBias;
+                        work.ml[2 * piece + 1] = l;
+                    }
+                }
+                if (x < NX) advance(w);
+                c0 = 0;
+            }
+            if (!ok && lane == 0) atomicOr(v.err, KVQ_DEVERR_TIMEOUT);
+        } else if (warp == 2) {
+            if (lane == 0) {  // for the merge: the unit that this CTA starts in
+                const ChunkWalk w = begin();
+                int32_t *e = work.first + 8 * blockIdx.x;
+                e[0] = w.b;
+                e[1] = w.h;
+                e[2] = w.u;
+                e[3] = x0 - s_start[3];  // its first step
+                e[4] = w.steps;
+                e[5] = span;
+            }
+            __syncwarp();
+        }
+    } else if (threadIdx.x == 0) {
+        work.first[8 * blockIdx.x + 4] = 0;  // nothing starts here
+    }
+    t5_fence_before();
+    __syncthreads();
+    t5_fence_after();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tm), "r"(512));
+}
+
+// Merge of the pieces.  Block (c, group of 8 rows): the unit that CTA c starts in, if CTA c - 1 began it.
+template <int NS, int DT>
+__global__ void __launch_bounds__(256)
+    paged_chunk_merge(const PagedAttnParams p, const ChunkWork work, const int rows_per_unit) {
+    using X = typename Act<DT>::type;
+    constexpr int D = NS * kSlice, DQ = D / 4;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    const int c = blockIdx.x + 1;
+    const int32_t *e = work.first + 8 * c;
+    const int steps = e[4];
+    if (steps == 0) return;
+    const int b = e[0], h = e[1], u = e[2], u0 = e[3], span = e[5];
+    const long long here = static_cast<long long>(c) * span;
+    if (u0 == here || u0 < here - span) return;  // the unit starts with CTA c, or before CTA c - 1
+    const PagedSeq s = paged_seq(p.v, b);
+    const int cl = (u0 + steps - 1) / span;  // last CTA with a piece
+    const int pieces = cl - (c - 1) + 1;
+    const int first_slot = 2 * (c - 1) + (u0 == here - span ? 0 : 1);
+    for (int item = threadIdx.x; item < 8 * DQ; item += blockDim.x) {
+        const int row = blockIdx.y * 8 + item / DQ, col = item % DQ;
+        const long long rr = static_cast<long long>(u) * rows_per_unit + row;
+        if (rr >= static_cast<long long>(s.n) * p.G) continue;
+        float M = -CUDART_INF_F, L = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kAt = 4;
+        for (int i0 = 0; i0 < pieces; i0 += kAt) {
+            float pm[kAt], pl[kAt];
+            float4 po[kAt];
+#pragma unroll
+            for (int k = 0; k < kAt; ++k) {
+                pm[k] = -CUDART_INF_F;
+                pl[k] = 0.f;
+                po[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i0 + k < pieces) {
+                    const int slot = i0 + k == 0 ? first_slot : 2 * (c - 1 + i0 + k);
+                    const size_t at = static_cast<size_t>(slot) * rows_per_unit + row;
+                    pm[k] = __ldcg(work.ml + 2 * at);
+                    pl[k] = __ldcg(work.ml + 2 * at + 1);
+                    po[k] = __ldcg(reinterpret_cast<const float4 *>(work.o + at * D) + col);
+                }
+            }
+            float mn = M;
+#pragma unroll
+            for (int k = 0; k < kAt; ++k) mn = fmaxf(mn, pm[k]);
+            if (mn == -CUDART_INF_F) continue;
+            const float k0 = M == -CUDART_INF_F ? 0.f : chunk_ex2(M - mn);
+            a = make_float4(a.x * k0, a.y * k0, a.z * k0, a.w * k0);
+            L *= k0;
+#pragma unroll
+            for (int k = 0; k < kAt; ++k) {
+                const float q = pm[k] == -CUDART_INF_F ? 0.f : chunk_ex2(pm[k] - mn);
+                a = make_float4(fmaf(q, po[k].x, a.x), fmaf(q, po[k].y, a.y), fmaf(q, po[k].z, a.z), fmaf(q, po[k].w, a.w));
+                L = fmaf(q, pl[k], L);
+            }
+            M = mn;
+        }
+        const size_t orow = (static_cast<size_t>(s.first) + rr / p.G) * p.Hq + static_cast<size_t>(h) * p.G + rr % p.G;
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        Act<DT>::store4(static_cast<X *>(p.out) + orow * D + 4 * col, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
+        if (col == 0 && p.lse) p.lse[orow] = L > 0.f ? (M + __log2f(L)) * kChunkLn2 : -CUDART_INF_F;
+    }
+}
+
+template <int KT, int VT, int NS, int DT>
+cudaError_t launch_chunk_t(const PagedAttnParams &p, cudaStream_t stream) {
+    using C = ChunkCfg<KT, VT, NS>;
+    static bool configured[kPagedMaxDevices] = {};
+    int dev = 0, sms = 0;
+    cudaError_t e = paged_device(&dev, &sms);
+    if (e != cudaSuccess) return e;
+    if (!configured[dev]) {
+        e = cudaFuncSetAttribute(paged_chunk_kernel<KT, VT, NS, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess) return e;
+        configured[dev] = true;
+    }
+    const ChunkWork work = chunk_work(p.workspace, sms, C::ROWS, C::D, nullptr);
+    // sequences of one launch: their prefix sums fit shared memory, their steps 2^30
+    const long long units = (static_cast<long long>(p.v.max_q) * p.G + C::ROWS - 1) / C::ROWS;
+    const long long per_seq = units * ((p.v.max_len + C::NK) / C::NK) * p.v.Hkv;
+    const long long fit = (1ll << 30) / per_seq;
+    const int most = static_cast<int>(fit < kChunkMaxSeqs ? fit : kChunkMaxSeqs);
+    if (most < 1) return cudaErrorInvalidValue;
+    for (int b = 0; b < p.v.n_seqs; b += most) {
+        const PagedAttnParams q = paged_some(p, b, most);
+        e = launch_dependent(paged_chunk_kernel<KT, VT, NS, DT>, dim3(sms), C::THREADS, C::SMEM, stream, q, work);
+        if (e != cudaSuccess) return e;
+        if (sms == 1) continue;
+        e = launch_dependent(paged_chunk_merge<NS, DT>, dim3(sms - 1, C::ROWS / 8), 256, 0, stream, q, work, static_cast<int>(C::ROWS));
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+template <int DT>
+cudaError_t launch_chunk_dt(int type_k, int type_v, int D, const PagedAttnParams &p, cudaStream_t s) {
+#define KVQ_CHUNK_CASE(KT_, VT_)                                                  \
+    if (type_k == KT_ && type_v == VT_) {                                         \
+        if (D == kSlice) return launch_chunk_t<KT_, VT_, 1, DT>(p, s);            \
+        if (D == 2 * kSlice) return launch_chunk_t<KT_, VT_, 2, DT>(p, s);        \
+    }
+    KVQ_CHUNK_CASE(KVQ_F16, KVQ_F16)
+    KVQ_CHUNK_CASE(KVQ_Q8_0, KVQ_Q8_0)
+    KVQ_CHUNK_CASE(KVQ_Q8_0, KVQ_Q4_0)
+    KVQ_CHUNK_CASE(KVQ_Q4_0, KVQ_Q4_0)
+#undef KVQ_CHUNK_CASE
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+}  // namespace kvq

@@ -1,0 +1,18 @@
+// kvq_paged_chunk_f16.cu -- paged attention of many queries per sequence, f16 activations.
+#include "kvq_paged_chunk.cuh"
+
+namespace kvq {
+
+cudaError_t launch_paged_chunk_f16(int type_k, int type_v, int D, const PagedAttnParams &p, cudaStream_t s) {
+    return launch_chunk_dt<KVQ_DT_F16>(type_k, type_v, D, p, s);
+}
+
+cudaError_t paged_chunk_workspace(int D, size_t *bytes) {
+    int dev = 0, sms = 0;
+    const cudaError_t e = paged_device(&dev, &sms);
+    if (e != cudaSuccess) return e;
+    (void)chunk_work(nullptr, sms, D == kSlice ? ChunkCfg<KVQ_F16, KVQ_F16, 1>::ROWS : ChunkCfg<KVQ_F16, KVQ_F16, 2>::ROWS, D, bytes);
+    return cudaSuccess;
+}
+
+}  // namespace kvq

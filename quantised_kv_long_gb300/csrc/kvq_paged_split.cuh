@@ -332,19 +332,25 @@ struct Walk {
     int tiles, steps, units, groups;  // of the sequence
 };
 
+// sequence b, without tokens if it belongs to the chunk kernel
+__device__ __forceinline__ PagedSeq split_seq(const PagedAttnParams &p, int b) {
+    PagedSeq s = paged_seq(p.v, b);
+    if (s.n >= p.split_below) s.n = 0;
+    return s;
+}
 template <int TPS>
-__device__ __forceinline__ void walk_seq(Walk &w, const PagedView &v, int G, int b) {
-    const PagedSeq s = paged_seq(v, b);
+__device__ __forceinline__ void walk_seq(Walk &w, const PagedAttnParams &p, int b) {
+    const PagedSeq s = split_seq(p, b);
     w.b = b;
     w.tiles = (s.len + kTileRows - 1) / kTileRows;
     w.steps = (w.tiles + TPS - 1) / TPS;
-    w.groups = (s.n * G + kRows - 1) / kRows;
-    w.units = w.groups * v.Hkv;
+    w.groups = (s.n * p.G + kRows - 1) / kRows;
+    w.units = w.groups * p.v.Hkv;
 }
 // position at step x of all steps; pre[b] <= x < pre[n_seqs]
 template <int TPS>
-__device__ __forceinline__ void walk_to(Walk &w, const PagedView &v, int G, const int *pre, int x) {
-    int lo = 0, hi = v.n_seqs;  // last b with pre[b] <= x (it has steps, for pre[b + 1] > x)
+__device__ __forceinline__ void walk_to(Walk &w, const PagedAttnParams &p, const int *pre, int x) {
+    int lo = 0, hi = p.v.n_seqs;  // last b with pre[b] <= x (it has steps, for pre[b + 1] > x)
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (pre[mid] <= x)
@@ -352,19 +358,19 @@ __device__ __forceinline__ void walk_to(Walk &w, const PagedView &v, int G, cons
         else
             hi = mid;
     }
-    walk_seq<TPS>(w, v, G, lo);
+    walk_seq<TPS>(w, p, lo);
     const int r = x - pre[lo];
     w.unit = r / w.steps;
     w.t = r - w.unit * w.steps;
 }
 // the first step of the next unit (a step follows: the caller counts)
 template <int TPS>
-__device__ __forceinline__ void walk_next_unit(Walk &w, const PagedView &v, int G, const int *pre) {
+__device__ __forceinline__ void walk_next_unit(Walk &w, const PagedAttnParams &p, const int *pre) {
     w.t = 0;
     if (++w.unit < w.units) return;
     int b = w.b + 1;
     while (pre[b + 1] == pre[b]) ++b;
-    walk_seq<TPS>(w, v, G, b);
+    walk_seq<TPS>(w, p, b);
     w.unit = 0;
 }
 
@@ -410,7 +416,7 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
         int sum = 0;
         for (int b = b0; b < b1; ++b) {
             Walk w;
-            walk_seq<TPS>(w, v, p.G, b);
+            walk_seq<TPS>(w, p, b);
             pre[b] = sum;
             sum += w.steps * w.units;
             if (blockIdx.x == 0 && !paged_seq(v, b).ok) paged_error(v);
@@ -503,7 +509,7 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
         uint8_t *ring = smem + warp * (C::SLOTS * C::STEP);
         // ---- the issuing side runs SLOTS steps ahead ----
         Walk iss;
-        walk_to<TPS>(iss, v, p.G, pre, x0);
+        walk_to<TPS>(iss, p, pre, x0);
         cur = iss;
         int ix = x0;                // its step
         int pg = 0, tip = 0;        // table entry and tile in page of its first tile
@@ -556,7 +562,7 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
                 tip += TPS;
                 while (tip >= v.page_tiles) tip -= v.page_tiles, ++pg;
             } else {
-                walk_next_unit<TPS>(iss, v, p.G, pre);
+                walk_next_unit<TPS>(iss, p, pre);
                 pg = tip = 0;
             }
             look_up();
@@ -576,7 +582,7 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
             if (fresh) {  // a new unit: its queries, empty accumulators
                 fresh = false;
                 seg0 = x;
-                const PagedSeq s = paged_seq(v, cur.b);
+                const PagedSeq s = split_seq(p, cur.b);
                 const int h = cur.unit / cur.groups, qg = cur.unit - h * cur.groups;
                 rows = unit_rows(p, s, h, qg);
                 len = s.len;
@@ -710,7 +716,7 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
                     write_out();
                 else
                     write_piece(gw * 2 + 1);
-                walk_next_unit<TPS>(cur, v, p.G, pre);
+                walk_next_unit<TPS>(cur, p, pre);
                 fresh = true;
             }
         }
@@ -802,7 +808,7 @@ __global__ void __launch_bounds__(NS * 32 * kMergeWays)
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int row = blockIdx.x % kRows, rest = blockIdx.x / kRows;
     const int qg = rest % max_groups, h = (rest / max_groups) % p.v.Hkv, b = rest / max_groups / p.v.Hkv;
-    const PagedSeq s = paged_seq(p.v, b);
+    const PagedSeq s = split_seq(p, b);
     const int groups = (s.n * p.G + kRows - 1) / kRows;
     if (qg >= groups) return;
     const UnitRows rows = unit_rows(p, s, h, qg);
@@ -884,47 +890,15 @@ __global__ void __launch_bounds__(NS * 32 * kMergeWays)
     if (c == 0 && p.lse) p.lse[orow] = L > 0.f ? (M + __log2f(L)) * kSplitLn2 : -CUDART_INF_F;
 }
 
-constexpr int kSplitMaxDevices = 64;
-
-// SMs of the current device, looked up once
-inline cudaError_t split_sms(int dev, int *n) {
-    static int cached[kSplitMaxDevices] = {};
-    if (dev < 0 || dev >= kSplitMaxDevices) return cudaErrorInvalidDevice;
-    if (cached[dev] == 0) {
-        int c = 0;
-        const cudaError_t e = cudaDeviceGetAttribute(&c, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess) return e;
-        cached[dev] = c > 0 ? c : 1;
-    }
-    *n = cached[dev];
-    return cudaSuccess;
-}
-
-template <class... A, class... B>
-cudaError_t launch_dependent(void (*kernel)(A...), dim3 grid, int threads, int smem, cudaStream_t s, B... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 constexpr int kSplitMaxWarps = 16;
 
 template <int KT, int VT, int NS, int DT>
 cudaError_t launch_split_t(const PagedAttnParams &p, cudaStream_t stream) {
     using C = SplitCfg<KT, VT, NS, DT>;
     static_assert(C::WARPS <= kSplitMaxWarps, "workspace");
-    static bool configured[kSplitMaxDevices] = {};
+    static bool configured[kPagedMaxDevices] = {};
     int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = split_sms(dev, &sms);
+    cudaError_t e = paged_device(&dev, &sms);
     if (e != cudaSuccess) return e;
     if (!configured[dev]) {
         e = cudaFuncSetAttribute(paged_split_kernel<KT, VT, NS, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
@@ -932,21 +906,15 @@ cudaError_t launch_split_t(const PagedAttnParams &p, cudaStream_t stream) {
         configured[dev] = true;
     }
     const SplitWork work = split_work(p.workspace, 2 * kSplitMaxWarps * sms);
-    const int max_groups = (p.v.max_q * p.G + kRows - 1) / kRows;
+    const int max_q = p.v.max_q < p.split_below ? p.v.max_q : p.split_below - 1;
+    const int max_groups = static_cast<int>((static_cast<long long>(max_q) * p.G + kRows - 1) / kRows);
     // sequences of one launch: their prefix sums fit shared memory, their steps 2^30
     const long long per_seq = static_cast<long long>(p.v.max_len + kTileRows - 1) / kTileRows * p.v.Hkv * max_groups;
     const long long fit = per_seq > 0 ? (1ll << 30) / per_seq : kSplitMaxSeqs;
     const int most = static_cast<int>(fit < kSplitMaxSeqs ? fit : kSplitMaxSeqs);
     if (most < 1) return cudaErrorInvalidValue;
     for (int b = 0; b < p.v.n_seqs; b += most) {
-        PagedAttnParams q = p;
-        q.v.n_seqs = p.v.n_seqs - b < most ? p.v.n_seqs - b : most;
-        q.v.lens += b;
-        q.v.table += static_cast<size_t>(b) * p.v.stride;
-        if (p.v.cu_q)
-            q.v.cu_q += b;
-        else
-            q.v.token0 = p.v.token0 + b;
+        const PagedAttnParams q = paged_some(p, b, most);
         e = launch_dependent(paged_split_kernel<KT, VT, NS, DT>, dim3(sms), C::THREADS, C::SMEM, stream, q, work);
         if (e != cudaSuccess) return e;
         const long long units = static_cast<long long>(q.v.n_seqs) * p.v.Hkv * max_groups * kRows;

@@ -9,8 +9,7 @@ cudaError_t launch_paged_split_f32(int type_k, int type_v, int D, const PagedAtt
 
 cudaError_t paged_split_workspace(int D, size_t *bytes) {
     int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = split_sms(dev, &sms);
+    const cudaError_t e = paged_device(&dev, &sms);
     if (e != cudaSuccess) return e;
     *bytes = split_work_bytes(2 * kSplitMaxWarps * sms, D);
     return cudaSuccess;
