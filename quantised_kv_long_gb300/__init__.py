@@ -491,30 +491,34 @@ class PagedCache:
             self.handle = None
 
     def _batch(self, block_table, lens, cu_q, max_q, max_len, n_tokens):
-        n_seqs = lens.numel()
-        _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == n_seqs and
-              block_table.stride(1) == 1 and block_table.device == self.device, "block_table: int32 [n_seqs, width] on the cache's device")
-        _need(lens.dtype == torch.int32 and lens.is_contiguous() and lens.device == self.device,
-              "lens: contiguous int32 [n_seqs] on the cache's device")
+        n_seqs, device, shape, strides = lens.numel(), self.device, block_table.shape, block_table.stride()
+        if not (block_table.dtype == torch.int32 and len(shape) == 2 and shape[0] == n_seqs and strides[1] == 1 and
+                block_table.device == device):
+            raise ValueError("block_table: int32 [n_seqs, width] on the cache's device")
+        if not (lens.dtype == torch.int32 and lens.device == device and lens.is_contiguous()):
+            raise ValueError("lens: contiguous int32 [n_seqs] on the cache's device")
         if cu_q is None:
             _need(n_tokens >= n_seqs, "without cu_q every sequence has one token")
-            max_q = 1
+            max_q, cu = 1, 0
         else:
-            _need(cu_q.dtype == torch.int32 and cu_q.is_contiguous() and cu_q.numel() == n_seqs + 1 and
-                  cu_q.device == self.device, "cu_q: contiguous int32 [n_seqs + 1] on the cache's device")
-            max_q = max(1, n_tokens) if max_q is None else max_q
-        width = block_table.shape[1]
-        return PagedBatch(n_seqs, n_tokens, max_q, width * self.page_size if max_len is None else max_len,
-                          0 if cu_q is None else cu_q.data_ptr(), lens.data_ptr(), block_table.data_ptr(), width,
-                          max(width, block_table.stride(0)))
+            if not (cu_q.dtype == torch.int32 and cu_q.numel() == n_seqs + 1 and cu_q.device == device and cu_q.is_contiguous()):
+                raise ValueError("cu_q: contiguous int32 [n_seqs + 1] on the cache's device")
+            cu = cu_q.data_ptr()
+            if max_q is None:
+                max_q = max(1, n_tokens)
+        width = shape[1]
+        return PagedBatch(n_seqs, n_tokens, max_q, width * self.page_size if max_len is None else max_len, cu, lens.data_ptr(),
+                          block_table.data_ptr(), width, max(width, strides[0]))
 
     def _rows(self, t, heads, what, dtype=None):
         """Packed rows [n_tokens, heads, D] with contiguous heads and values: (pointer, token stride)."""
-        _need(t.device == self.device and t.dim() == 3 and t.shape[2] == self.head_dim and (heads is None or t.shape[1] == heads) and
-              t.dtype in DTYPE_IDS and (dtype is None or t.dtype == dtype), f"{what}: [n_tokens, heads, {self.head_dim}] of one activation type on the cache's device")
-        width = t.shape[1] * self.head_dim
-        _need(t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == self.head_dim), f"{what}: heads and values must be contiguous")
-        return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else width)
+        shape, strides, dim = t.shape, t.stride(), self.head_dim
+        if not (len(shape) == 3 and shape[2] == dim and (heads is None or shape[1] == heads) and t.device == self.device and
+                (t.dtype == dtype if dtype is not None else t.dtype in DTYPE_IDS)):
+            raise ValueError(f"{what}: [n_tokens, heads, {dim}] of one activation type on the cache's device")
+        if strides[2] != 1 or (strides[1] != dim and shape[1] != 1):
+            raise ValueError(f"{what}: heads and values must be contiguous")
+        return t.data_ptr(), (strides[0] if shape[0] > 1 else shape[1] * dim)
 
     def _call(self, stream, fn, *args):
         """fn(*args) with the cache's device, and `stream` if given, current."""
@@ -525,6 +529,10 @@ class PagedCache:
             with torch.cuda.device(self.device):
                 return fn(*args)
         return fn(*args)
+
+    def _stream(self):
+        # the handle alone: torch.cuda.current_stream() also makes a Stream object, 3 us a call
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
 
     def append(self, k, v, block_table, lens, cu_q=None, max_q=None, max_len=None, rope=None, positions=None, q=None,
                q_out=None, stream=None):
@@ -560,7 +568,7 @@ class PagedCache:
                 qop, qos = self._rows(result, hq, "q_out", k.dtype)
                 _need(result.shape[0] == n, "q_out and q have the same tokens")
         _check(lib.kvq_paged_append(self.handle, ctypes.byref(batch), kp, vp, DTYPE_IDS[k.dtype], ks, vs, ra, qp, hq, qs, qop,
-                                    qos, torch.cuda.current_stream().cuda_stream), "kvq_paged_append")
+                                    qos, self._stream()), "kvq_paged_append")
         return result
 
     def gather(self, block_table, lens, n_tokens, cu_q=None, max_q=None, max_len=None, dtype=torch.float16, stream=None):
@@ -575,7 +583,7 @@ class PagedCache:
         k = torch.empty(shape, dtype=dtype, device=self.device)
         v = torch.empty(shape, dtype=dtype, device=self.device)
         _check(lib.kvq_paged_gather(self.handle, ctypes.byref(batch), k.data_ptr(), v.data_ptr(), DTYPE_IDS[dtype],
-                                    torch.cuda.current_stream().cuda_stream), "kvq_paged_gather")
+                                    self._stream()), "kvq_paged_gather")
         return k, v
 
     def attention(self, q, block_table, lens, cu_q=None, max_q=None, max_len=None, scale=None, out=None, return_lse=False,
@@ -604,7 +612,7 @@ class PagedCache:
         _check(lib.kvq_paged_attention(self.handle, ctypes.byref(batch), qp, dt, hq, qs,
                                        1.0 / math.sqrt(d) if scale is None else scale, workspace.data_ptr(),
                                        workspace.numel() * workspace.element_size(), out.data_ptr(),
-                                       0 if lse is None else lse.data_ptr(), torch.cuda.current_stream().cuda_stream),
+                                       0 if lse is None else lse.data_ptr(), self._stream()),
                "kvq_paged_attention")
         return (out, lse) if return_lse else out
 
@@ -627,6 +635,6 @@ class PagedCache:
 
     def _read_error(self):
         e = ctypes.c_int32()
-        _check(lib.kvq_paged_read_error(self.handle, torch.cuda.current_stream().cuda_stream, ctypes.byref(e)),
+        _check(lib.kvq_paged_read_error(self.handle, self._stream(), ctypes.byref(e)),
                "kvq_paged_read_error")
         return e.value

@@ -35,6 +35,14 @@ constexpr float kChunkDrift = 4.0f, kChunkBias = 2.0f;
 // ---- tcgen05 and tensor memory (inline PTX) ----
 __device__ __forceinline__ void t5_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void t5_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+// One lane of a converged warp, always the same.  MMAs are issued under this predicate in code that the
+// whole warp runs: issued from a branch on the thread index, whose operands the compiler cannot keep in
+// uniform registers, every tcgen05.mma took 97 cycles whatever its N (measured; 32 for N = 64 this way).
+__device__ __forceinline__ bool t5_elect() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(r));
+    return r != 0;
+}
 // shared-memory operand without swizzle: 8-row x 16-byte core matrices, `lbo` bytes apart along K
 // and `sbo` along M or N
 __device__ __forceinline__ uint64_t t5_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
@@ -184,7 +192,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
     __shared__ int s_start[4];                       // sequence, head, unit, step of this CTA's first step
     __shared__ int s_ok[8], s_exp[8][2];             // per block: copied tiles; exponents of K^ and V^
     __shared__ uint32_t s_tmem;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const PagedView &v = p.v;
     const int G = p.G;
 
@@ -288,7 +296,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
         }
     }
     __syncthreads();
-    const uint32_t tm = s_tmem;
+    const uint32_t tm = __shfl_sync(0xffffffffu, s_tmem, 0);
 
     // every role walks the same segments: [c0, c1) are the steps of unit (b, h, u) in this CTA
     auto begin = [&]() {
@@ -373,75 +381,76 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
             __syncwarp();
         } else if (warp == 1) {
             // ---------------- MMA issue ----------------
-            if (lane == 0) {
-                constexpr uint32_t ID_S = t5_idesc(C::M, NK), ID_O = t5_idesc(C::M, D);
-                const uint64_t qd = t5_desc(smem_u32(smem + C::OFF_Q), 128, D * 16);
-                uint64_t kd[C::KB], vd[C::VB];
-                for (int i = 0; i < C::KB; ++i) kd[i] = t5_desc(smem_u32(smem + C::OFF_K + i * C::KHAT), 128, D * 16);
-                for (int i = 0; i < C::VB; ++i) vd[i] = t5_desc(smem_u32(smem + C::OFF_V + i * C::VHAT), 128, NK * 16);
-                auto qk = [&](int t, int x) {  // S_t = Q_t K^(x)^T
-                    const uint64_t b = kd[x % C::KB];
-                    const uint32_t d = tm + C::T_S + t * NK;
+            constexpr uint32_t ID_S = t5_idesc(C::M, NK), ID_O = t5_idesc(C::M, D);
+            const uint64_t qd = t5_desc(smem_u32(smem + C::OFF_Q), 128, D * 16);
+            const uint64_t kd = t5_desc(smem_u32(smem + C::OFF_K), 128, D * 16), vd = t5_desc(smem_u32(smem + C::OFF_V), 128, NK * 16);
+            auto qk = [&](int t, int x, bool free_k) {  // S_t = Q_t K^(x)^T
+                const uint64_t b = kd + (x % C::KB) * (C::KHAT / 16);
+                if (t5_elect()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         if (t == 0)
-                            t5_mma_ts(d, tm + C::T_Q + 8 * k, b + 16 * k, ID_S, k > 0);
+                            t5_mma_ts(tm + C::T_S, tm + C::T_Q + 8 * k, b + 16 * k, ID_S, k > 0);
                         else
-                            t5_mma_ss(d, qd + 16 * k, b + 16 * k, ID_S, k > 0);
+                            t5_mma_ss(tm + C::T_S + NK, qd + 16 * k, b + 16 * k, ID_S, k > 0);
                     }
                     t5_commit(s_ready + t);
-                };
-                auto pv = [&](int t, int x, bool start) {  // O_t += P_t V^(x)
-                    const uint64_t b = vd[x % C::VB];
+                    if (free_k) t5_commit(k_free + x % C::KB);
+                }
+                __syncwarp();
+            };
+            auto pv = [&](int t, int x, bool start, bool free_v) {  // O_t += P_t V^(x)
+                const uint64_t b = vd + (x % C::VB) * (C::VHAT / 16);
+                const uint32_t o = tm + C::T_O + t * D, a = tm + C::T_P + t * (NK / 2);
+                if (t5_elect()) {
 #pragma unroll
-                    for (int k = 0; k < NK / 16; ++k)
-                        t5_mma_ts(tm + C::T_O + t * D, tm + C::T_P + t * (NK / 2) + 8 * k, b + 16 * k, ID_O, !start || k > 0);
+                    for (int k = 0; k < NK / 16; ++k) t5_mma_ts(o, a + 8 * k, b + 16 * k, ID_O, !start || k > 0);
                     t5_commit(pv_done + t);
-                };
-                ChunkWalk w = begin();
-                int c0 = s_start[3], x = 0;
-                int done[2] = {0, 0}, segs[2] = {0, 0};  // steps and segments of each tile so far (phases of its barriers)
-                bool ok = true;
-                while (x < NX && ok) {
-                    const int n = min(w.steps - c0, NX - x);  // steps of this segment
-                    const int nt = NT == 2 && tile_rows(w, 1) > 0 ? 2 : 1;
-                    ok = mbar_wait(k_ready + x % C::KB, (x / C::KB) & 1);
+                    if (free_v) t5_commit(v_free + x % C::VB);
+                }
+                __syncwarp();
+            };
+            ChunkWalk w = begin();
+            int c0 = s_start[3], x = 0;
+            int done[2] = {0, 0}, segs[2] = {0, 0};  // steps and segments of each tile so far (phases of its barriers)
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, int phase) { return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1)) != 0; };
+            while (x < NX && ok) {
+                const int n = min(w.steps - c0, NX - x);  // steps of this segment
+                const int nt = NT == 2 && tile_rows(w, 1) > 0 ? 2 : 1;
+                ok = wait(k_ready + x % C::KB, x / C::KB);
+                for (int t = 0; t < nt && ok; ++t) {
+                    // a tile's queries are staged once its last segment's O has been read
+                    ok = wait(q_ready + t, segs[t]++);
+                    t5_fence_after();
+                    if (ok) qk(t, x, t == nt - 1);
+                }
+                for (int c = 0; c < n && ok; ++c) {
+                    const bool more = c + 1 < n;
+                    if (more) ok = wait(k_ready + (x + 1) % C::KB, (x + 1) / C::KB);
                     for (int t = 0; t < nt && ok; ++t) {
-                        // a tile's queries are staged once its last segment's O has been read
-                        ok = mbar_wait(q_ready + t, segs[t]++ & 1);
-                        t5_fence_after();
-                        if (ok) qk(t, x);
-                    }
-                    if (ok) t5_commit(k_free + x % C::KB);
-                    for (int c = 0; c < n && ok; ++c) {
-                        const bool more = c + 1 < n;
-                        if (more) ok = mbar_wait(k_ready + (x + 1) % C::KB, ((x + 1) / C::KB) & 1);
-                        for (int t = 0; t < nt && ok; ++t) {
-                            if (more) {
-                                ok = mbar_wait(s_free + t, done[t] & 1);
-                                t5_fence_after();
-                                if (!ok) break;
-                                qk(t, x + 1);
-                                if (t == nt - 1) t5_commit(k_free + (x + 1) % C::KB);
-                            }
-                            if (t == 0) ok = mbar_wait(v_ready + x % C::VB, (x / C::VB) & 1);
-                            ok = ok && mbar_wait(p_ready + t, done[t] & 1);
+                        if (more) {
+                            ok = wait(s_free + t, done[t]);
                             t5_fence_after();
                             if (!ok) break;
-                            pv(t, x, c == 0);
-                            if (t == nt - 1) t5_commit(v_free + x % C::VB);
-                            ++done[t];
+                            qk(t, x + 1, t == nt - 1);
                         }
-                        ++x;
+                        if (t == 0) ok = wait(v_ready + x % C::VB, x / C::VB);
+                        ok = ok && wait(p_ready + t, done[t]);
+                        t5_fence_after();
+                        if (!ok) break;
+                        pv(t, x, c == 0, t == nt - 1);
+                        ++done[t];
                     }
-                    if (x < NX && ok) advance(w);
-                    c0 = 0;
+                    ++x;
                 }
-                if (!ok) atomicOr(v.err, KVQ_DEVERR_TIMEOUT);
-                t5_commit(&drain);  // every MMA has completed before tensor memory is freed
-                (void)mbar_wait(&drain, 0);
+                if (x < NX && ok) advance(w);
+                c0 = 0;
             }
+            if (!ok && lane == 0) atomicOr(v.err, KVQ_DEVERR_TIMEOUT);
+            if (t5_elect()) t5_commit(&drain);  // every MMA has completed before tensor memory is freed
             __syncwarp();
+            (void)mbar_wait(&drain, 0);
         } else if (warp >= C::CONV0) {
             // ---------------- converters: codes -> K^, V^ ----------------
             const int cw = warp - C::CONV0;
