@@ -9,12 +9,17 @@
 // per SM), so ragged and causal work is even whatever the lengths.  A unit cut by a span boundary
 // leaves pieces (m, l, o) in the workspace, which a second kernel merges.
 //
-// A step, by warps: one thread streams the block's tile records into a ring (one bulk copy per run of
-// tiles in a page); eight warps turn codes into f16 operands K^ (keys x D) and V^ (D x keys) in
-// shared memory, once for all rows of the unit; one thread issues S = Q K^T and O += P V^; four warps
-// per tile hold one row per thread: running maximum, weights, P into tensor memory, and the rescale
-// of O when the maximum moves by more than kChunkDrift.  S of the next block is computed while the
-// softmax of this one runs (S and P have their own columns).
+// A step, by warps: warp 0 streams the block's tile records into a ring; half of the converter warps
+// turn key codes into the f16 operand K^ (keys x D) in shared memory, the other half value codes into
+// V^ (D x keys), once for all rows of the unit; warps 1 and 2 issue S = Q K^T and O += P V^ (one per
+// tile, or one per product where there is one tile); four warps per tile hold one row per thread:
+// running maximum, weights, P into tensor memory, and the rescale of O when the maximum moves by more
+// than kChunkDrift.  S of the next block is computed while the softmax of this one runs (S and P have
+// their own columns).
+//
+// Orders.  The values of K^ and Q sit in the order 0, 2, 1, 3 within each four (as the bytes of a code
+// word come out), and the rows of V^ (columns of O) in the order 0, 2, .., 14, 1, 3, .., 15 within each
+// sixteen, so that a warp's stores of V^ fill whole core matrices; the epilogue puts them back.
 //
 // Rounding.  Q is f16 after scaling each row by a power of two (exact for f16 and for bf16 in range).
 // K^ and V^ are scale x code rounded once to f16 (2^-11), P is f16 (2^-11); S, O, the maxima and
@@ -29,8 +34,8 @@ namespace kvq {
 namespace {
 
 constexpr float kChunkLn2 = 0.69314718055994530942f, kChunkLog2e = 1.44269504088896340736f;
-// weights are 2^(s - m + kChunkBias) <= 2^(kChunkBias + kChunkDrift), times 2^e <= 2^9 in f16
-constexpr float kChunkDrift = 4.0f, kChunkBias = 2.0f;
+// weights are 2^(s - m) <= 2^kChunkDrift, times 2^e <= 2^11 in f16
+constexpr float kChunkDrift = 4.0f;
 
 // ---- tcgen05 and tensor memory (inline PTX) ----
 __device__ __forceinline__ void t5_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
@@ -38,10 +43,15 @@ __device__ __forceinline__ void t5_fence_after() { asm volatile("tcgen05.fence::
 // One lane of a converged warp, always the same.  MMAs are issued under this predicate in code that the
 // whole warp runs: issued from a branch on the thread index, whose operands the compiler cannot keep in
 // uniform registers, every tcgen05.mma took 97 cycles whatever its N (measured; 32 for N = 64 this way).
+// Operands that depend on values loaded from memory go through t5_uniform for the same reason.
 __device__ __forceinline__ bool t5_elect() {
     uint32_t r;
     asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(r));
     return r != 0;
+}
+__device__ __forceinline__ uint32_t t5_uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ uint64_t t5_plus(uint64_t desc, uint32_t bytes) {  // a descriptor `bytes` further on
+    return (desc & 0xffffffff00000000ull) | t5_uniform(static_cast<uint32_t>(desc) + (bytes >> 4));
 }
 // shared-memory operand without swizzle: 8-row x 16-byte core matrices, `lbo` bytes apart along K
 // and `sbo` along M or N
@@ -97,6 +107,36 @@ __device__ __forceinline__ float chunk_ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// fp32 pairs, one instruction each
+__device__ __forceinline__ float2 pair_fma(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n .reg .b64 ra, rb, rc, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n mov.b64 rc, {%6, %7};\n"
+        " fma.rn.f32x2 rd, ra, rb, rc;\n mov.b64 {%0, %1}, rd;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 pair_add(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 ra, rb, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n add.rn.f32x2 rd, ra, rb;\n"
+        " mov.b64 {%0, %1}, rd;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 pair_mul(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 ra, rb, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n mul.rn.f32x2 rd, ra, rb;\n"
+        " mov.b64 {%0, %1}, rd;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 __device__ __forceinline__ uint32_t perm(uint32_t a, uint32_t b, uint32_t sel) {
     uint32_t d;
     asm("prmt.b32 %0, %1, %2, %3;\n" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
@@ -130,6 +170,7 @@ struct ChunkCfg {
     static_assert(T_Q + D / 2 <= 512, "tensor memory");
     static_assert(STAGES >= 2 && SMEM <= LIMIT, "shared memory");
     static constexpr int SOFT0 = 4, CONV0 = SOFT0 + 4 * NT, CONV_WARPS = 8;  // first softmax / converter warp
+    static constexpr int HALF = CONV_WARPS / 2;                              // converters of K^, and of V^
     static constexpr int WARPS = CONV0 + CONV_WARPS;
     static constexpr int THREADS = WARPS * 32;
 };
@@ -187,7 +228,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
     constexpr int D = C::D, NK = C::NK, NT = C::NT, ROWS = C::ROWS;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t raw_full[4], raw_empty[4], k_ready[2], k_free[2], v_ready[2], v_free[2];
-    __shared__ __align__(8) uint64_t s_ready[2], s_free[2], p_ready[2], pv_done[2], q_ready[2], drain;
+    __shared__ __align__(8) uint64_t s_ready[2], s_free[2], p_ready[2], pv_done[2], q_ready[2], drain[2];
     __shared__ int s_pre[kChunkMaxSeqs + 1];
     __shared__ int s_start[4];                       // sequence, head, unit, step of this CTA's first step
     __shared__ int s_ok[8], s_exp[8][2];             // per block: copied tiles; exponents of K^ and V^
@@ -202,17 +243,18 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
             mbar_init(raw_empty + i, C::CONV_WARPS);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(k_ready + i, C::CONV_WARPS);
-            mbar_init(k_free + i, 1);
-            mbar_init(v_ready + i, C::CONV_WARPS);
-            mbar_init(v_free + i, 1);
+            mbar_init(k_ready + i, C::HALF);
+            mbar_init(k_free + i, NT);
+            mbar_init(v_ready + i, C::HALF);
+            mbar_init(v_free + i, NT);
             mbar_init(s_ready + i, 1);
             mbar_init(s_free + i, 4);
             mbar_init(p_ready + i, 4);
             mbar_init(pv_done + i, 1);
             mbar_init(q_ready + i, 4);
         }
-        mbar_init(&drain, 1);
+        mbar_init(drain, 1);
+        mbar_init(drain + 1, 1);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -329,154 +371,163 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
     if (NX > 0) {
         if (warp == 0) {
             // ---------------- copies ----------------
-            if (lane == 0) {
-                ChunkWalk w = begin();
-                int t = s_start[3], issued = 0;
-                bool ok = true;
-                const size_t page_bytes = static_cast<size_t>(v.page_tiles) * T::BYTES;
-                for (int x = 0; x < NX; ++x) {
-                    const int st = x % C::STAGES, use = x / C::STAGES;
-                    if (use > 0 && !mbar_wait(raw_empty + st, (use - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    const int tile0 = t * C::TILES, tiles = (w.s.len + kTileRows - 1) / kTileRows;
-                    const int32_t *row = v.table + static_cast<size_t>(w.b) * v.stride;
-                    const uint8_t *src[C::TILES];
-                    int got = 0;
-                    int e = tile0 / v.page_tiles, q = tile0 - e * v.page_tiles;
-#pragma unroll
-                    for (int i = 0; i < C::TILES; ++i) {
-                        src[i] = nullptr;
-                        if (tile0 + i < tiles) {
-                            const int page = __ldg(row + e);
-                            if (page >= 0 && page < v.n_pages) {
-                                src[i] = v.pool + (static_cast<size_t>(page) * v.Hkv + w.h) * page_bytes + static_cast<size_t>(q) * T::BYTES;
-                                got |= 1 << i;
-                            } else {
-                                paged_error(v);
-                            }
-                        }
-                        if (++q == v.page_tiles) q = 0, ++e;
-                    }
+            // lane i < 4 has tile i of the block; its page number is looked up one step ahead
+            ChunkWalk w = begin();
+            int t = s_start[3], issued = 0, page = -1, tile = 0, tiles = 0;
+            const size_t page_bytes = static_cast<size_t>(v.page_tiles) * T::BYTES;
+            const bool one_page = v.page_tiles % C::TILES == 0;  // a block never crosses a page: one copy
+            auto look_up = [&]() {
+                tiles = (w.s.len + kTileRows - 1) / kTileRows;
+                tile = t * C::TILES + (lane & (C::TILES - 1));
+                page = tile < tiles ? __ldg(v.table + static_cast<size_t>(w.b) * v.stride + tile / v.page_tiles) : -1;
+            };
+            look_up();
+            bool ok = true;
+            for (int x = 0; x < NX; ++x) {
+                const int st = x % C::STAGES, use = x / C::STAGES;
+                if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(raw_empty + st, (use - 1) & 1));
+                if (!ok) break;
+                const bool in = page >= 0 && page < v.n_pages;
+                if (!in && tile < tiles && lane < C::TILES) paged_error(v);
+                const int got = __ballot_sync(0xffffffffu, in) & ((1 << C::TILES) - 1);
+                if (lane == 0) {
                     s_ok[x & 7] = got;
                     mbar_arrive_expect_tx(raw_full + st, static_cast<uint32_t>(__popc(got) * T::BYTES));
-                    uint8_t *dst = smem + st * C::STAGE;
-#pragma unroll
-                    for (int i = 0; i < C::TILES; ++i)
-                        if (src[i]) bulk_g2s(dst + i * T::BYTES, src[i], T::BYTES, raw_full + st);
-                    issued = x + 1;
-                    if (++t == w.steps && x + 1 < NX) {
+                }
+                __syncwarp();
+                const uint8_t *src = v.pool + (static_cast<size_t>(page) * v.Hkv + w.h) * page_bytes +
+                                     static_cast<size_t>(tile % v.page_tiles) * T::BYTES;
+                if (one_page) {
+                    if (lane == 0 && got) bulk_g2s(smem + st * C::STAGE, src, __popc(got) * T::BYTES, raw_full + st);
+                } else if (in && lane < C::TILES) {
+                    bulk_g2s(smem + st * C::STAGE + lane * T::BYTES, src, T::BYTES, raw_full + st);
+                }
+                issued = x + 1;
+                if (x + 1 < NX) {
+                    if (++t == w.steps) {
                         advance(w);
                         t = 0;
                     }
+                    look_up();
                 }
-                if (!ok) atomicOr(v.err, KVQ_DEVERR_TIMEOUT);
-                for (int i = 0; i < C::STAGES; ++i)  // every copy lands before the memory is freed
-                    if (i < issued) {
-                        const int lastx = (issued - 1 - i) / C::STAGES;  // last use of stage i
-                        (void)mbar_wait(raw_full + i, lastx & 1);
-                    }
             }
+            if (!ok && lane == 0) atomicOr(v.err, KVQ_DEVERR_TIMEOUT);
+            for (int i = 0; i < C::STAGES; ++i)  // every copy lands before the memory is freed
+                if (i < issued) (void)mbar_wait(raw_full + i, ((issued - 1 - i) / C::STAGES) & 1);
             __syncwarp();
-        } else if (warp == 1) {
+        } else if (warp == 1 || warp == 2) {
             // ---------------- MMA issue ----------------
             constexpr uint32_t ID_S = t5_idesc(C::M, NK), ID_O = t5_idesc(C::M, D);
             const uint64_t qd = t5_desc(smem_u32(smem + C::OFF_Q), 128, D * 16);
             const uint64_t kd = t5_desc(smem_u32(smem + C::OFF_K), 128, D * 16), vd = t5_desc(smem_u32(smem + C::OFF_V), 128, NK * 16);
-            auto qk = [&](int t, int x, bool free_k) {  // S_t = Q_t K^(x)^T
-                const uint64_t b = kd + (x % C::KB) * (C::KHAT / 16);
+            const int tile = NT == 2 ? warp - 1 : 0;
+            auto qk = [&](int x) {  // S = Q K^(x)^T of this warp's tile
+                const uint64_t b = t5_plus(kd, (x % C::KB) * C::KHAT);
                 if (t5_elect()) {
+                    if (NT == 1 || tile == 0) {
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        if (t == 0)
-                            t5_mma_ts(tm + C::T_S, tm + C::T_Q + 8 * k, b + 16 * k, ID_S, k > 0);
-                        else
-                            t5_mma_ss(tm + C::T_S + NK, qd + 16 * k, b + 16 * k, ID_S, k > 0);
+                        for (int k = 0; k < D / 16; ++k) t5_mma_ts(tm + C::T_S, tm + C::T_Q + 8 * k, b + 16 * k, ID_S, k > 0);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) t5_mma_ss(tm + C::T_S + NK, qd + 16 * k, b + 16 * k, ID_S, k > 0);
                     }
-                    t5_commit(s_ready + t);
-                    if (free_k) t5_commit(k_free + x % C::KB);
+                    t5_commit(s_ready + tile);
+                    t5_commit(k_free + x % C::KB);
                 }
                 __syncwarp();
             };
-            auto pv = [&](int t, int x, bool start, bool free_v) {  // O_t += P_t V^(x)
-                const uint64_t b = vd + (x % C::VB) * (C::VHAT / 16);
-                const uint32_t o = tm + C::T_O + t * D, a = tm + C::T_P + t * (NK / 2);
+            auto pv = [&](int x, bool start) {  // O += P V^(x)
+                const uint64_t b = t5_plus(vd, (x % C::VB) * C::VHAT);
+                const uint32_t o = t5_uniform(tm + C::T_O + tile * D), a = t5_uniform(tm + C::T_P + tile * (NK / 2));
+                const uint32_t add = t5_uniform(start ? 0u : 1u);
                 if (t5_elect()) {
 #pragma unroll
-                    for (int k = 0; k < NK / 16; ++k) t5_mma_ts(o, a + 8 * k, b + 16 * k, ID_O, !start || k > 0);
-                    t5_commit(pv_done + t);
-                    if (free_v) t5_commit(v_free + x % C::VB);
+                    for (int k = 0; k < NK / 16; ++k) t5_mma_ts(o, a + 8 * k, b + 16 * k, ID_O, k > 0 ? 1u : add);
+                    t5_commit(pv_done + tile);
+                    t5_commit(v_free + x % C::VB);
                 }
                 __syncwarp();
             };
             ChunkWalk w = begin();
-            int c0 = s_start[3], x = 0;
-            int done[2] = {0, 0}, segs[2] = {0, 0};  // steps and segments of each tile so far (phases of its barriers)
+            int c0 = s_start[3], x = 0, done = 0, segs = 0;  // done, segs: steps and segments of the tile (barrier phases)
             bool ok = true;
-            auto wait = [&](uint64_t *bar, int phase) { return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1)) != 0; };
+            auto wait = [&](uint64_t *bar, int phase) {
+                const bool got = __all_sync(0xffffffffu, mbar_wait(bar, phase & 1)) != 0;
+                t5_fence_after();
+                return got;
+            };
+            auto k_wait = [&](int y) { return wait(k_ready + y % C::KB, y / C::KB); };
+            auto v_wait = [&](int y) { return wait(v_ready + y % C::VB, y / C::VB); };
             while (x < NX && ok) {
                 const int n = min(w.steps - c0, NX - x);  // steps of this segment
-                const int nt = NT == 2 && tile_rows(w, 1) > 0 ? 2 : 1;
-                ok = wait(k_ready + x % C::KB, x / C::KB);
-                for (int t = 0; t < nt && ok; ++t) {
-                    // a tile's queries are staged once its last segment's O has been read
-                    ok = wait(q_ready + t, segs[t]++);
-                    t5_fence_after();
-                    if (ok) qk(t, x, t == nt - 1);
-                }
-                for (int c = 0; c < n && ok; ++c) {
-                    const bool more = c + 1 < n;
-                    if (more) ok = wait(k_ready + (x + 1) % C::KB, (x + 1) / C::KB);
-                    for (int t = 0; t < nt && ok; ++t) {
-                        if (more) {
-                            ok = wait(s_free + t, done[t]);
-                            t5_fence_after();
-                            if (!ok) break;
-                            qk(t, x + 1, t == nt - 1);
+                if (NT == 2 && tile_rows(w, tile) == 0) {
+                    // nothing for this tile: its share of the buffers' releases, in step with the converters
+                    for (int c = 0; c < n && ok; ++c, ++x) {
+                        ok = k_wait(x) && v_wait(x);
+                        if (lane == 0) {
+                            mbar_arrive(k_free + x % C::KB);
+                            mbar_arrive(v_free + x % C::VB);
                         }
-                        if (t == 0) ok = wait(v_ready + x % C::VB, x / C::VB);
-                        ok = ok && wait(p_ready + t, done[t]);
-                        t5_fence_after();
-                        if (!ok) break;
-                        pv(t, x, c == 0, t == nt - 1);
-                        ++done[t];
                     }
-                    ++x;
+                } else {
+                    for (int c = 0; c < n && ok; ++c, ++x, ++done) {
+                        if constexpr (NT == 2) {  // both products of one tile
+                            if (c == 0) {
+                                // the queries are staged once the last segment's O has been read
+                                ok = k_wait(x) && wait(q_ready + tile, segs++);
+                                if (ok) qk(x);
+                            }
+                            if (c + 1 < n && ok) {
+                                ok = k_wait(x + 1) && wait(s_free + tile, done);
+                                if (ok) qk(x + 1);
+                            }
+                            ok = ok && v_wait(x) && wait(p_ready + tile, done);
+                            if (ok) pv(x, c == 0);
+                        } else if (warp == 1) {
+                            ok = k_wait(x) && (c == 0 ? wait(q_ready, segs++) : wait(s_free, done - 1));
+                            if (ok) qk(x);
+                        } else {
+                            ok = v_wait(x) && wait(p_ready, done);
+                            if (ok) pv(x, c == 0);
+                        }
+                    }
                 }
                 if (x < NX && ok) advance(w);
                 c0 = 0;
             }
             if (!ok && lane == 0) atomicOr(v.err, KVQ_DEVERR_TIMEOUT);
-            if (t5_elect()) t5_commit(&drain);  // every MMA has completed before tensor memory is freed
+            // every MMA has completed before tensor memory is freed
+            if (t5_elect()) t5_commit(drain + warp - 1);
             __syncwarp();
-            (void)mbar_wait(&drain, 0);
+            (void)mbar_wait(drain + warp - 1, 0);
         } else if (warp >= C::CONV0) {
-            // ---------------- converters: codes -> K^, V^ ----------------
-            const int cw = warp - C::CONV0;
-            constexpr int NCW = C::CONV_WARPS;
+            // ---------------- converters: codes -> K^ (first half of the warps), V^ (second half) ----------------
+            const bool keys = warp < C::CONV0 + C::HALF;
+            const int cw = warp - C::CONV0 - (keys ? 0 : C::HALF);
             const uint32_t magic = 0x64006400u;  // f16 1024 | bits = 1024 + bits
-            const __half2 k1024 = __float2half2_rn(1024.0f), k1032 = __float2half2_rn(1032.0f);
-            const __half2 k16th = __float2half2_rn(0.0625f), km72 = __float2half2_rn(-72.0f);
-            auto q8pair = [&](uint32_t word, uint32_t sel_mag, uint32_t sel_sign) {  // two sign-magnitude bytes
-                const uint32_t m = (perm(word, 0u, sel_mag) & 0x007f007fu) | magic;
-                const uint32_t sg = perm(word, 0u, sel_sign) & 0x80008000u;
-                return u32_as_h2(h2_as_u32(__hsub2(u32_as_h2(m), k1024)) | sg);
-            };
+            const __half2 k1032 = __float2half2_rn(1032.0f), k16th = __float2half2_rn(0.0625f), km72 = __float2half2_rn(-72.0f);
+            const __half2 k2to14 = __float2half2_rn(16384.0f);
+            // bytes 0, 2 / 1, 3 of a word of q8_0 codes, times 2^-10: f16 subnormals times 2^14, exact
+            auto q8_02 = [&](uint32_t w) { return __hmul2(u32_as_h2(perm(w, 0u, 0xA280u) & 0x807f807fu), k2to14); };
+            auto q8_13 = [&](uint32_t w) { return __hmul2(u32_as_h2(perm(w, 0u, 0xB391u) & 0x807f807fu), k2to14); };
+            // bytes 0, 2 of a word of q4_0 codes: low or high nibbles less 8
             auto q4lo = [&](uint32_t x) { return __hsub2(u32_as_h2((x & 0x000f000fu) | magic), k1032); };
             auto q4hi = [&](uint32_t x) { return __hfma2(u32_as_h2((x & 0x00f000f0u) | magic), k16th, km72); };
             auto both = [](uint32_t w, int upper) { return perm(w, 0u, upper ? 0x3232u : 0x1010u); };  // one half twice
-            // rows of tile i of block x in use
+            // rows of tile i of the block in use
             auto rows_of = [&](int len, int t, int got, int i) {
                 return ((got >> i) & 1) ? max(0, min(kTileRows, len - (t * C::TILES + i) * kTileRows)) : 0;
             };
-            // exponent e >= 0 with the block's largest |scale| cmax 2^-e at most 2^14, over the rows in use
-            auto block_exp = [&](const uint8_t *st, int off, float cmax, int len, int t, int got) {
+            // Exponent e >= 0 with |value| 2^-e below 2^14 (q4_0) or 2^12 (q8_0, whose scale meets codes times
+            // 2^-10) over the block's rows in use; at most 11.
+            auto block_exp = [&](const uint8_t *sc, int type, int len, int t, int got) {
+                const float cmax = type == KVQ_Q8_0 ? 127.f : 8.f;
+                const int most = type == KVQ_Q8_0 ? 12 : 14;
                 uint32_t m = 0;
 #pragma unroll
                 for (int k = 0; k < NS; ++k) {
                     const int gi = k * 32 + lane, i = gi / (8 * NS), in = gi % (8 * NS);  // tile, 16-byte group of its scales
-                    uint4 w = *reinterpret_cast<const uint4 *>(st + i * T::BYTES + off + in * 16);
+                    uint4 w = *reinterpret_cast<const uint4 *>(sc + i * T::BYTES + in * 16);
                     const int use = rows_of(len, t, got, i), ka = 2 * ((in & 7) >> 1);
                     if (use < kTileRows) {
                         auto cut = [&](uint32_t x, int r) { return r >= use ? 0u : (r + 1 >= use ? (x & 0xffffu) : x); };
@@ -486,12 +537,12 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
                     const __half2 b = __hmax2(__habs2(u32_as_h2(w.z)), __habs2(u32_as_h2(w.w)));
                     m = h2_as_u32(__hmax2(u32_as_h2(m), __hmax2(a, b)));
                 }
-                float2 f = __half22float2(u32_as_h2(m));
+                const float2 f = __half22float2(u32_as_h2(m));
                 float top = fmaxf(f.x, f.y) * cmax;
-                if (!__any_sync(0xffffffffu, top > 16384.f)) return 0;
+                if (!__any_sync(0xffffffffu, top > static_cast<float>(1 << most))) return 0;
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                return min(9, max(0, ilogbf(top) - 13));
+                return min(11, max(0, ilogbf(top) - (most - 1)));
             };
             auto pow2 = [](int e) { return __int_as_float((127 + e) << 23); };
 
@@ -502,42 +553,46 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
                 const int sg = x % C::STAGES;
                 const uint8_t *st = smem + sg * C::STAGE;
                 ok = mbar_wait(raw_full + sg, (x / C::STAGES) & 1);
-                if (x >= C::KB) ok = mbar_wait(k_free + x % C::KB, (x / C::KB - 1) & 1) && ok;
+                const int buf = keys ? x % C::KB : x % C::VB, use_no = keys ? x / C::KB : x / C::VB;
+                if (use_no > 0) ok = mbar_wait((keys ? k_free : v_free) + buf, (use_no - 1) & 1) && ok;
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 const int got = s_ok[x & 7], len = w.s.len;
-                int ek = 0, ev = 0;
-                if constexpr (KT != KVQ_F16) ek = block_exp(st, T::OFF_KS, KT == KVQ_Q8_0 ? 127.f : 8.f, len, t, got);
-                if constexpr (VT != KVQ_F16) ev = block_exp(st, T::OFF_VS, VT == KVQ_Q8_0 ? 127.f : 8.f, len, t, got);
-                if (cw == 0 && lane == 0) {
-                    s_exp[x & 7][0] = ek;
-                    s_exp[x & 7][1] = ev;
-                }
-                // ---- K^ ----
-                {
-                    uint8_t *kh = smem + C::OFF_K + (x % C::KB) * C::KHAT;
-                    const __half2 fk = __float2half2_rn(pow2(-ek));
+                if (keys) {
+                    // ---- K^: rows past the sequence's end may become anything; their scores are masked ----
+                    int e = 0;
+                    if constexpr (KT != KVQ_F16) e = block_exp(st + T::OFF_KS, KT, len, t, got);
+                    if (cw == 0 && lane == 0) s_exp[x & 7][0] = e;
+                    if (cw == 1) {  // the softmax warps need V^'s exponent with S, perhaps before V^ is made
+                        int ev = 0;
+                        if constexpr (VT != KVQ_F16) ev = block_exp(st + T::OFF_VS, VT, len, t, got);
+                        if (lane == 0) s_exp[x & 7][1] = ev;
+                    }
+                    uint8_t *kh = smem + C::OFF_K + buf * C::KHAT;
+                    const __half2 fk = __float2half2_rn(pow2(KT == KVQ_Q8_0 ? 10 - e : -e));
                     const int n = lane >> 2, jd = lane & 3;  // key n (and n + 8) of the tile, 4-value group jd
-                    auto put = [&](int key, int dim, __half2 c01, __half2 c23, __half2 d2) {
-                        *reinterpret_cast<uint2 *>(kh + core_at(key, dim, D)) = make_uint2(h2_as_u32(__hmul2(c01, d2)), h2_as_u32(__hmul2(c23, d2)));
+                    uint8_t *lane_at = kh + (jd >> 1) * 128 + n * 16 + (jd & 1) * 8;  // core_at(n, 4 jd, D)
+                    auto put = [&](int at, __half2 c02, __half2 c13, __half2 d2) {
+                        *reinterpret_cast<uint2 *>(lane_at + at) = make_uint2(h2_as_u32(__hmul2(c02, d2)), h2_as_u32(__hmul2(c13, d2)));
                     };
+                    // core_at(16 i + n + 8 s, dim + 4 jd, D) less lane_at, for dim a multiple of 16
+                    auto at = [](int i, int s8, int dim) { return (2 * i + s8) * (D * 16) + dim * 16; };
                     if constexpr (KT == KVQ_Q8_0) {
-#pragma unroll
-                        for (int wu = cw; wu < C::TILES * NS * 4; wu += NCW) {
-                            const int ts = wu >> 2, b = wu & 3, i = ts / NS, sl = ts % NS;
+#pragma unroll 4
+                        for (int wu = cw; wu < C::TILES * NS * 4; wu += C::HALF) {
+                            const int ts = wu >> 2, b = wu & 3, i = ts / NS, sl = ts % NS, dim = sl * kSlice + 32 * b;
                             const uint8_t *tile = st + i * T::BYTES;
                             const uint4 c = *reinterpret_cast<const uint4 *>(tile + sl * 2048 + (b * 32 + lane) * 16);
                             const uint2 sc = *reinterpret_cast<const uint2 *>(tile + T::OFF_KS + sl * kScaleTile + (n >> 1) * 32 + b * 8);
-                            const int k0 = i * kTileRows + n, dim = sl * kSlice + 32 * b + 4 * jd;
                             const __half2 da = __hmul2(u32_as_h2(both(sc.x, n & 1)), fk), db = __hmul2(u32_as_h2(both(sc.y, n & 1)), fk);
-                            put(k0, dim, q8pair(c.x, 0x4140u, 0x1404u), q8pair(c.x, 0x4342u, 0x3424u), da);
-                            put(k0, dim + 16, q8pair(c.y, 0x4140u, 0x1404u), q8pair(c.y, 0x4342u, 0x3424u), da);
-                            put(k0 + 8, dim, q8pair(c.z, 0x4140u, 0x1404u), q8pair(c.z, 0x4342u, 0x3424u), db);
-                            put(k0 + 8, dim + 16, q8pair(c.w, 0x4140u, 0x1404u), q8pair(c.w, 0x4342u, 0x3424u), db);
+                            put(at(i, 0, dim), q8_02(c.x), q8_13(c.x), da);
+                            put(at(i, 0, dim + 16), q8_02(c.y), q8_13(c.y), da);
+                            put(at(i, 1, dim), q8_02(c.z), q8_13(c.z), db);
+                            put(at(i, 1, dim + 16), q8_02(c.w), q8_13(c.w), db);
                         }
                     } else if constexpr (KT == KVQ_Q4_0) {
-#pragma unroll
-                        for (int wu = cw; wu < C::TILES * NS * 2; wu += NCW) {
+#pragma unroll 2
+                        for (int wu = cw; wu < C::TILES * NS * 2; wu += C::HALF) {
                             const int ts = wu >> 1, b2 = wu & 1, i = ts / NS, sl = ts % NS;
                             const uint8_t *tile = st + i * T::BYTES;
                             const uint4 c = *reinterpret_cast<const uint4 *>(tile + sl * 1024 + (b2 * 32 + lane) * 16);
@@ -545,43 +600,40 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
                             const uint32_t cs[4] = {c.x, c.y, c.z, c.w}, ss[4] = {sc.x, sc.y, sc.z, sc.w};
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {  // block 2 b2 + q / 2, key n + 8 (q % 2)
-                                const int key = i * kTileRows + n + 8 * (q & 1), dim = sl * kSlice + 64 * b2 + 32 * (q >> 1) + 4 * jd;
+                                const int dim = sl * kSlice + 64 * b2 + 32 * (q >> 1);
                                 const __half2 d2 = __hmul2(u32_as_h2(both(ss[q], n & 1)), fk);
-                                const uint32_t w01 = perm(cs[q], 0u, 0x4140u), w23 = perm(cs[q], 0u, 0x4342u);
-                                put(key, dim, q4lo(w01), q4lo(w23), d2);
-                                put(key, dim + 16, q4hi(w01), q4hi(w23), d2);
+                                const uint32_t odd = cs[q] >> 8;
+                                put(at(i, q & 1, dim), q4lo(cs[q]), q4lo(odd), d2);
+                                put(at(i, q & 1, dim + 16), q4hi(cs[q]), q4hi(odd), d2);
                             }
                         }
                     } else {
-#pragma unroll
-                        for (int wu = cw; wu < C::TILES * NS * 8; wu += NCW) {
-                            const int ts = wu >> 3, ch = wu & 7, i = ts / NS, sl = ts % NS;
+#pragma unroll 4
+                        for (int wu = cw; wu < C::TILES * NS * 8; wu += C::HALF) {
+                            const int ts = wu >> 3, ch = wu & 7, i = ts / NS, sl = ts % NS, dim = sl * kSlice + 32 * (ch >> 1);
                             const uint4 c = *reinterpret_cast<const uint4 *>(st + i * T::BYTES + sl * 4096 + (ch * 32 + lane) * 16);
-                            const int key = i * kTileRows + n + 8 * (ch & 1), dim = sl * kSlice + 32 * (ch >> 1) + 4 * jd;
-                            *reinterpret_cast<uint2 *>(kh + core_at(key, dim, D)) = make_uint2(perm(c.x, c.y, 0x5410u), perm(c.x, c.y, 0x7632u));
-                            *reinterpret_cast<uint2 *>(kh + core_at(key, dim + 16, D)) = make_uint2(perm(c.z, c.w, 0x5410u), perm(c.z, c.w, 0x7632u));
+                            *reinterpret_cast<uint2 *>(lane_at + at(i, ch & 1, dim)) = make_uint2(c.x, c.y);
+                            *reinterpret_cast<uint2 *>(lane_at + at(i, ch & 1, dim + 16)) = make_uint2(c.z, c.w);
                         }
                     }
-                    smem_to_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(k_ready + x % C::KB);
-                }
-                // ---- V^: rows past the sequence's end may hold any bits and become 0 ----
-                if (x >= C::VB) ok = __all_sync(0xffffffffu, mbar_wait(v_free + x % C::VB, (x / C::VB - 1) & 1));
-                if (!ok) break;
-                {
-                    uint8_t *vh = smem + C::OFF_V + (x % C::VB) * C::VHAT;
-                    const __half2 fv = __float2half2_rn(pow2(-ev));
+                } else {
+                    // ---- V^: rows past the sequence's end may hold any bits and become 0 ----
+                    int e = 0;
+                    if constexpr (VT != KVQ_F16) e = block_exp(st + T::OFF_VS, VT, len, t, got);
+                    uint8_t *vh = smem + C::OFF_V + buf * C::VHAT;
+                    const __half2 fv = __float2half2_rn(pow2(VT == KVQ_Q8_0 ? 10 - e : -e));
                     const int np = lane >> 2, j = lane & 3;
-                    auto put = [&](int dim, int k0, __half2 ca, __half2 cb, __half2 da, __half2 db) {
-                        uint8_t *at = vh + core_at(dim, k0, NK);  // keys k0, k0 + 1 and k0 + 8, k0 + 9
-                        *reinterpret_cast<uint32_t *>(at) = h2_as_u32(__hmul2(ca, da));
-                        *reinterpret_cast<uint32_t *>(at + 128) = h2_as_u32(__hmul2(cb, db));
+                    uint8_t *lane_at = vh + np * 16 + j * 4;  // row np of a core matrix, keys 2j, 2j + 1
+                    // value dim + 2 np + odd of keys 16 i + 2j, + 1 (and + 8, + 9): row (dim / 8 + odd) * 8 + np
+                    auto at = [](int i, int dim, int odd) { return ((dim >> 3) + odd) * (NK * 16) + 2 * i * 128; };
+                    auto put = [&](int a, __half2 ca, __half2 cb, __half2 da, __half2 db) {
+                        *reinterpret_cast<uint32_t *>(lane_at + a) = h2_as_u32(__hmul2(ca, da));
+                        *reinterpret_cast<uint32_t *>(lane_at + a + 128) = h2_as_u32(__hmul2(cb, db));
                     };
                     auto cut = [&](uint32_t s2, int r, int use) { return r >= use ? 0u : (r + 1 >= use ? (s2 & 0xffffu) : s2); };
                     if constexpr (VT == KVQ_Q8_0) {
-#pragma unroll
-                        for (int wu = cw; wu < C::TILES * NS * 4; wu += NCW) {
+#pragma unroll 4
+                        for (int wu = cw; wu < C::TILES * NS * 4; wu += C::HALF) {
                             const int ts = wu >> 2, b = wu & 3, i = ts / NS, sl = ts % NS;
                             const uint8_t *tile = st + i * T::BYTES;
                             const uint4 c = *reinterpret_cast<const uint4 *>(tile + T::OFF_V + sl * 2048 + (b * 32 + lane) * 16);
@@ -590,48 +642,47 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
                             const __half2 da = __hmul2(u32_as_h2(cut(sc.x, 2 * j, use)), fv), db = __hmul2(u32_as_h2(cut(sc.y, 2 * j + 8, use)), fv);
                             const uint32_t cs[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                put(sl * kSlice + 32 * b + 16 * (q >> 1) + 2 * np + (q & 1), i * kTileRows + 2 * j, q8pair(cs[q], 0x4240u, 0x2404u),
-                                    q8pair(cs[q], 0x4341u, 0x3414u), da, db);
+                            for (int q = 0; q < 4; ++q) put(at(i, sl * kSlice + 32 * b + 16 * (q >> 1), q & 1), q8_02(cs[q]), q8_13(cs[q]), da, db);
                         }
                     } else if constexpr (VT == KVQ_Q4_0) {
-#pragma unroll
-                        for (int wu = cw; wu < C::TILES * NS * 2; wu += NCW) {
+#pragma unroll 2
+                        for (int wu = cw; wu < C::TILES * NS * 2; wu += C::HALF) {
                             const int ts = wu >> 1, b2 = wu & 1, i = ts / NS, sl = ts % NS;
                             const uint8_t *tile = st + i * T::BYTES;
                             const uint4 c = *reinterpret_cast<const uint4 *>(tile + T::OFF_V + sl * 1024 + (b2 * 32 + lane) * 16);
                             const uint4 sc = *reinterpret_cast<const uint4 *>(tile + T::OFF_VS + sl * kScaleTile + j * 32 + b2 * 16);
-                            const int use = rows_of(len, t, got, i), k0 = i * kTileRows + 2 * j;
+                            const int use = rows_of(len, t, got, i);
                             const __half2 d[4] = {__hmul2(u32_as_h2(cut(sc.x, 2 * j, use)), fv), __hmul2(u32_as_h2(cut(sc.y, 2 * j + 8, use)), fv),
                                                   __hmul2(u32_as_h2(cut(sc.z, 2 * j, use)), fv), __hmul2(u32_as_h2(cut(sc.w, 2 * j + 8, use)), fv)};
                             const uint32_t cs[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {  // block 2 b2 + q / 2, value 2 np + q % 2 (and + 16)
-                                const int dim = sl * kSlice + 64 * b2 + 32 * (q >> 1) + 2 * np + (q & 1);
-                                const uint32_t wa = perm(cs[q], 0u, 0x4240u), wb = perm(cs[q], 0u, 0x4341u);
-                                put(dim, k0, q4lo(wa), q4lo(wb), d[2 * (q >> 1)], d[2 * (q >> 1) + 1]);
-                                put(dim + 16, k0, q4hi(wa), q4hi(wb), d[2 * (q >> 1)], d[2 * (q >> 1) + 1]);
+                                const int dim = sl * kSlice + 64 * b2 + 32 * (q >> 1);
+                                const uint32_t odd = cs[q] >> 8;
+                                put(at(i, dim, q & 1), q4lo(cs[q]), q4lo(odd), d[2 * (q >> 1)], d[2 * (q >> 1) + 1]);
+                                put(at(i, dim + 16, q & 1), q4hi(cs[q]), q4hi(odd), d[2 * (q >> 1)], d[2 * (q >> 1) + 1]);
                             }
                         }
                     } else {
-#pragma unroll
-                        for (int wu = cw; wu < C::TILES * NS * 8; wu += NCW) {
+#pragma unroll 4
+                        for (int wu = cw; wu < C::TILES * NS * 8; wu += C::HALF) {
                             const int ts = wu >> 3, ch = wu & 7, i = ts / NS, sl = ts % NS;
                             const uint4 c = *reinterpret_cast<const uint4 *>(st + i * T::BYTES + T::OFF_V + sl * 4096 + (ch * 32 + lane) * 16);
-                            const int use = rows_of(len, t, got, i), dim = sl * kSlice + 32 * (ch >> 1) + 16 * (ch & 1) + 2 * np;
-                            uint8_t *at = vh + core_at(dim, i * kTileRows + 2 * j, NK);
-                            *reinterpret_cast<uint32_t *>(at) = cut(c.x, 2 * j, use);
-                            *reinterpret_cast<uint32_t *>(at + 128) = cut(c.y, 2 * j + 8, use);
-                            *reinterpret_cast<uint32_t *>(at + 16) = cut(c.z, 2 * j, use);  // dim is even: dim + 1 is the next row
-                            *reinterpret_cast<uint32_t *>(at + 144) = cut(c.w, 2 * j + 8, use);
+                            const int use = rows_of(len, t, got, i), dim = sl * kSlice + 32 * (ch >> 1) + 16 * (ch & 1);
+#pragma unroll
+                            for (int odd = 0; odd < 2; ++odd) {
+                                uint8_t *to = lane_at + at(i, dim, odd);
+                                *reinterpret_cast<uint32_t *>(to) = cut(odd ? c.z : c.x, 2 * j, use);
+                                *reinterpret_cast<uint32_t *>(to + 128) = cut(odd ? c.w : c.y, 2 * j + 8, use);
+                            }
                         }
                     }
-                    smem_to_async();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(v_ready + x % C::VB);
-                        mbar_arrive(raw_empty + sg);  // the stage has been read
-                    }
+                }
+                smem_to_async();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive((keys ? k_ready : v_ready) + buf);
+                    mbar_arrive(raw_empty + sg);  // this warp's part of the stage has been read
                 }
                 if (++t == w.steps && x + 1 < NX) {
                     advance(w);
@@ -680,8 +731,8 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             const float4 q4 = rv ? Act<DT>::load4(src + d0 + 4 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
-                            h[2 * e] = h2_as_u32(__floats2half2_rn(q4.x * up, q4.y * up));
-                            h[2 * e + 1] = h2_as_u32(__floats2half2_rn(q4.z * up, q4.w * up));
+                            h[2 * e] = h2_as_u32(__floats2half2_rn(q4.x * up, q4.z * up));
+                            h[2 * e + 1] = h2_as_u32(__floats2half2_rn(q4.y * up, q4.w * up));
                         }
                         if (tile == 0) {
                             t5_st16(trow + C::T_Q + d0 / 2, h);
@@ -728,10 +779,14 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
                             for (int k = 0; k < NK; ++k)
                                 if (key0 + k > lim || !((got >> (k / kTileRows)) & 1)) s[k] = -CUDART_INF_F;
                         }
-                        float mx = s[0];
+                        float mq[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                        for (int k = 1; k < NK; ++k) mx = fmaxf(mx, s[k]);
-                        mx *= f;
+                        for (int k = 4; k + 8 <= NK; k += 8)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) mq[e] = max3(mq[e], s[k + 2 * e], s[k + 2 * e + 1]);
+                        mq[0] = max3(mq[0], s[NK - 4], s[NK - 3]);
+                        mq[1] = max3(mq[1], s[NK - 2], s[NK - 1]);
+                        const float mx = fmaxf(max3(mq[0], mq[1], mq[2]), mq[3]) * f;
                         const bool need = mx > m_run + kChunkDrift;
                         float alpha = 1.f;
                         if (need) {
@@ -739,15 +794,21 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
                             m_run = mx;
                             l *= alpha;
                         }
-                        const float base = (m_run == -CUDART_INF_F ? 0.f : m_run) - kChunkBias;
+                        // weights times 2^ev (the values were stored times 2^-ev)
+                        const float base = (m_run == -CUDART_INF_F ? 0.f : m_run) - static_cast<float>(ev);
+                        const float2 f2 = make_float2(f, f), nb2 = make_float2(-base, -base);
+                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                         uint32_t pw[NK / 2];
-                        const float fe = __int_as_float((127 + ev) << 23);
 #pragma unroll
                         for (int k = 0; k < NK / 2; ++k) {
-                            const float a = chunk_ex2(fmaf(s[2 * k], f, -base)), b = chunk_ex2(fmaf(s[2 * k + 1], f, -base));
-                            l += a + b;
-                            pw[k] = h2_as_u32(__floats2half2_rn(a * fe, b * fe));
+                            float2 a = pair_fma(make_float2(s[2 * k], s[2 * k + 1]), f2, nb2);
+                            a.x = chunk_ex2(a.x);
+                            a.y = chunk_ex2(a.y);
+                            sum[k & 1] = pair_add(sum[k & 1], a);
+                            pw[k] = h2_as_u32(__floats2half2_rn(a.x, a.y));
                         }
+                        sum[0] = pair_add(sum[0], sum[1]);
+                        l += (sum[0].x + sum[0].y) * __int_as_float((127 - ev) << 23);
                         // P and O are free once the previous block's P V^ is done
                         if (c > 0) ok = __all_sync(0xffffffffu, mbar_wait(pv_done + tile, (done - 1) & 1));
                         if (!ok) break;
@@ -759,7 +820,11 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
                                 t5_ld32(tO + d0, o);
                                 t5_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                for (int e = 0; e < 32; e += 2) {
+                                    const float2 y = pair_mul(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), make_float2(alpha, alpha));
+                                    o[e] = __float_as_uint(y.x);
+                                    o[e + 1] = __float_as_uint(y.y);
+                                }
                                 t5_st32(tO + d0, o);
                             }
                         }
@@ -784,11 +849,13 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
                             t5_wait_ld();
                             if (rv)
 #pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    Act<DT>::store4(dst + d0 + 4 * e, make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
-                                                                                  __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv));
+                                for (int e = 0; e < 8; ++e) {
+                                    const int i0 = 16 * (e >> 2) + 2 * (e & 3);
+                                    Act<DT>::store4(dst + d0 + 4 * e, make_float4(__uint_as_float(o[i0]) * inv, __uint_as_float(o[i0 + 8]) * inv,
+                                                                                  __uint_as_float(o[i0 + 1]) * inv, __uint_as_float(o[i0 + 9]) * inv));
+                                }
                         }
-                        if (rv && p.lse) p.lse[orow] = l > 0.f ? (m_run - kChunkBias + __log2f(l)) * kChunkLn2 : -CUDART_INF_F;
+                        if (rv && p.lse) p.lse[orow] = l > 0.f ? (m_run + __log2f(l)) * kChunkLn2 : -CUDART_INF_F;
                     } else {
                         // the first segment of the CTA, or its last
                         const size_t piece = (static_cast<size_t>(2) * blockIdx.x + (x - n > 0 ? 1 : 0)) * ROWS + tile * C::M + r;
@@ -800,10 +867,12 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
                             t5_wait_ld();
                             if (rv)
 #pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    *reinterpret_cast<uint4 *>(dst + d0 + 4 * e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                                for (int e = 0; e < 8; ++e) {
+                                    const int i0 = 16 * (e >> 2) + 2 * (e & 3);
+                                    *reinterpret_cast<uint4 *>(dst + d0 + 4 * e) = make_uint4(o[i0], o[i0 + 8], o[i0 + 1], o[i0 + 9]);
+                                }
                         }
-                        work.ml[2 * piece] = m_run == -CUDART_INF_F ? -CUDART_INF_F : m_run - kChunkBias;
+                        work.ml[2 * piece] = m_run;
                         work.ml[2 * piece + 1] = l;
                     }
                 }
@@ -811,7 +880,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
                 c0 = 0;
             }
             if (!ok && lane == 0) atomicOr(v.err, KVQ_DEVERR_TIMEOUT);
-        } else if (warp == 2) {
+        } else if (warp == 3) {
             if (lane == 0) {  // for the merge: the unit that this CTA starts in
                 const ChunkWalk w = begin();
                 int32_t *e = work.first + 8 * blockIdx.x;
