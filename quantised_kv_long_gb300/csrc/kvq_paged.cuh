@@ -77,6 +77,22 @@ __device__ __forceinline__ uint8_t *paged_tile(const PagedView &v, int b, int h,
     return v.pool + ((static_cast<size_t>(page) * v.Hkv + h) * v.page_tiles + t % v.page_tiles) * T::BYTES;
 }
 
+// Bounded wait for a barrier phase: false after about two seconds.  The hardware holds the warp for up
+// to 20 us per try, so that a waiting warp takes few issue slots from the working ones.
+__device__ __forceinline__ bool paged_wait(uint64_t *bar, uint32_t parity) {
+    const uint32_t addr = smem_u32(bar);
+    const long long t0 = clock64();
+    while (true) {
+        uint32_t ok;
+        asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n selp.u32 %0, 1, 0, p;\n}\n"
+                     : "=r"(ok)
+                     : "r"(addr), "r"(parity)
+                     : "memory");
+        if (ok) return true;
+        if (clock64() - t0 > kWaitCycles) return false;
+    }
+}
+
 // ---- activations: fp32, f16, bf16 ----
 template <int DT>
 struct Act;

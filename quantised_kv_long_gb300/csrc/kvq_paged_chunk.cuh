@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
             bool ok = true;
             for (int x = 0; x < NX; ++x) {
                 const int st = x % C::STAGES, use = x / C::STAGES;
-                if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(raw_empty + st, (use - 1) & 1));
+                if (use > 0) ok = __all_sync(0xffffffffu, paged_wait(raw_empty + st, (use - 1) & 1));
                 if (!ok) break;
                 const bool in = page >= 0 && page < v.n_pages;
                 if (!in && tile < tiles && lane < C::TILES) paged_error(v);
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
             }
             if (!ok && lane == 0) atomicOr(v.err, KVQ_DEVERR_TIMEOUT);
             for (int i = 0; i < C::STAGES; ++i)  // every copy lands before the memory is freed
-                if (i < issued) (void)mbar_wait(raw_full + i, ((issued - 1 - i) / C::STAGES) & 1);
+                if (i < issued) (void)paged_wait(raw_full + i, ((issued - 1 - i) / C::STAGES) & 1);
             __syncwarp();
         } else if (warp == 1 || warp == 2) {
             // ---------------- MMA issue ----------------
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
             int c0 = s_start[3], x = 0, done = 0, segs = 0;  // done, segs: steps and segments of the tile (barrier phases)
             bool ok = true;
             auto wait = [&](uint64_t *bar, int phase) {
-                const bool got = __all_sync(0xffffffffu, mbar_wait(bar, phase & 1)) != 0;
+                const bool got = __all_sync(0xffffffffu, paged_wait(bar, phase & 1)) != 0;
                 t5_fence_after();
                 return got;
             };
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
             // every MMA has completed before tensor memory is freed
             if (t5_elect()) t5_commit(drain + warp - 1);
             __syncwarp();
-            (void)mbar_wait(drain + warp - 1, 0);
+            (void)paged_wait(drain + warp - 1, 0);
         } else if (warp >= C::CONV0) {
             // ---------------- converters: codes -> K^ (first half of the warps), V^ (second half) ----------------
             const bool keys = warp < C::CONV0 + C::HALF;
@@ -552,9 +552,9 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
             for (int x = 0; x < NX && ok; ++x) {
                 const int sg = x % C::STAGES;
                 const uint8_t *st = smem + sg * C::STAGE;
-                ok = mbar_wait(raw_full + sg, (x / C::STAGES) & 1);
+                ok = paged_wait(raw_full + sg, (x / C::STAGES) & 1);
                 const int buf = keys ? x % C::KB : x % C::VB, use_no = keys ? x / C::KB : x / C::VB;
-                if (use_no > 0) ok = mbar_wait((keys ? k_free : v_free) + buf, (use_no - 1) & 1) && ok;
+                if (use_no > 0) ok = paged_wait((keys ? k_free : v_free) + buf, (use_no - 1) & 1) && ok;
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 const int got = s_ok[x & 7], len = w.s.len;
@@ -756,7 +756,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
                     x += n;
                 } else {
                     for (int c = 0; c < n && ok; ++c, ++x, ++done) {
-                        ok = __all_sync(0xffffffffu, mbar_wait(s_ready + tile, done & 1));
+                        ok = __all_sync(0xffffffffu, paged_wait(s_ready + tile, done & 1));
                         if (!ok) break;
                         t5_fence_after();
                         uint32_t su[NK];
@@ -810,7 +810,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
                         sum[0] = pair_add(sum[0], sum[1]);
                         l += (sum[0].x + sum[0].y) * __int_as_float((127 - ev) << 23);
                         // P and O are free once the previous block's P V^ is done
-                        if (c > 0) ok = __all_sync(0xffffffffu, mbar_wait(pv_done + tile, (done - 1) & 1));
+                        if (c > 0) ok = __all_sync(0xffffffffu, paged_wait(pv_done + tile, (done - 1) & 1));
                         if (!ok) break;
                         t5_fence_after();
                         if (c > 0 && __any_sync(0xffffffffu, need)) {
@@ -835,7 +835,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
                         if (lane == 0) mbar_arrive(p_ready + tile);
                     }
                     if (!ok) break;
-                    ok = __all_sync(0xffffffffu, mbar_wait(pv_done + tile, (done - 1) & 1));
+                    ok = __all_sync(0xffffffffu, paged_wait(pv_done + tile, (done - 1) & 1));
                     if (!ok) break;
                     t5_fence_after();
                     const bool whole = c0 == 0 && n == w.steps;

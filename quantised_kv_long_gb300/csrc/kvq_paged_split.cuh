@@ -602,12 +602,12 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
                 bias = kBias;
             }
             const uint8_t *st = ring + slot * C::STEP;
-            if (__any_sync(0xffffffffu, !mbar_wait(full + slot, phase))) {
+            if (__any_sync(0xffffffffu, !paged_wait(full + slot, phase))) {
                 // gave up: the outputs of the call are undefined and the error word says so.  Copies in
                 // flight land before the memory is used again.
                 if (lane == 0) atomicOr(v.err, KVQ_DEVERR_TIMEOUT);
                 for (; x < ix; ++x) {
-                    (void)mbar_wait(full + slot, phase);
+                    (void)paged_wait(full + slot, phase);
                     if (++slot == C::SLOTS) slot = 0, phase ^= 1u;
                 }
                 break;
