@@ -442,6 +442,148 @@ __device__ __forceinline__ void quantize_store(const float *x, uint8_t *codes, u
     quantize_store_vals<T, IS_V>(*reinterpret_cast<const float4 *>(x), codes, scales, kt, lane);
 }
 
+// One 32-value block of one row (block b of a slice, values x) by one thread: the arithmetic of
+// quantize_store_vals, operation for operation, without its shuffles.
+template <int T, bool IS_V>
+__device__ __forceinline__ void quantize_block_store(const float (&x)[kBlock], uint8_t *codes, uint8_t *scales,
+                                                     int kt, int b) {
+    const int n = kt & 7, st = kt >> 3;
+    int j, pos;
+    pair_slot(kt, j, pos);
+    if constexpr (T == KVQ_F16) {
+#pragma unroll
+        for (int g4 = 0; g4 < 8; ++g4) {
+            const __half h0 = __float2half_rn(x[4 * g4]), h1 = __float2half_rn(x[4 * g4 + 1]);
+            const __half h2 = __float2half_rn(x[4 * g4 + 2]), h3 = __float2half_rn(x[4 * g4 + 3]);
+            if constexpr (!IS_V) {
+                const uint2 w = make_uint2(h2_as_u32(__halves2half2(h0, h2)), h2_as_u32(__halves2half2(h1, h3)));
+                *reinterpret_cast<uint2 *>(codes + (2 * b + st) * 512 + (4 * n + (g4 & 3)) * 16 + (g4 >> 2) * 8) = w;
+            } else {
+                const __half hv[4] = {h0, h1, h2, h3};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 4 * g4 + e, r = i & 15, hh = i >> 4, n2 = r >> 1;
+                    *reinterpret_cast<__half *>(codes + (2 * b + hh) * 512 + (4 * n2 + j) * 16 + (r & 1) * 8 + pos * 2) =
+                        hv[e];
+                }
+            }
+        }
+        return;
+    }
+    if constexpr (T == KVQ_Q8_0) {
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < kBlock; ++i) amax = fmaxf(amax, fabsf(x[i]));
+        const float d = __fdiv_rn(amax, 127.0f);
+        const float id = d != 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
+        uint32_t c[kBlock];
+#pragma unroll
+        for (int i = 0; i < kBlock; ++i) {  // stored as a sign-magnitude byte
+            const int q = static_cast<int>(round_half_away(__fmul_rn(x[i], id)));
+            c[i] = static_cast<uint32_t>(q < 0 ? (0x80 | -q) : q) & 0xffu;
+        }
+        if constexpr (!IS_V) {
+#pragma unroll
+            for (int g4 = 0; g4 < 8; ++g4)
+                *reinterpret_cast<uint32_t *>(codes + b * 512 + (4 * n + (g4 & 3)) * 16 + (2 * st + (g4 >> 2)) * 4) =
+                    c[4 * g4] | (c[4 * g4 + 1] << 8) | (c[4 * g4 + 2] << 16) | (c[4 * g4 + 3] << 24);
+        } else {
+            const int vb = vword_byte(pos);
+#pragma unroll
+            for (int i = 0; i < kBlock; ++i) {
+                const int r = i & 15, hv = i >> 4, n2 = r >> 1;
+                codes[b * 512 + (4 * n2 + j) * 16 + ((r & 1) + 2 * hv) * 4 + vb] = static_cast<uint8_t>(c[i]);
+            }
+        }
+        *reinterpret_cast<__half *>(scales + j * 32 + b * 8 + pos * 2) = __float2half_rn(d);
+        return;
+    }
+    if constexpr (is_nibble_type(T)) {
+        int c[kBlock];
+        float d, lo = 0.f;
+        if constexpr (!has_min(T)) {
+            // value of largest magnitude, the lowest index on ties; d = m / -K; codes
+            // min(2K - 1, trunc(x / d + K + 1/2)) with K = 8 (q4_0) or 16 (q5_0)
+            constexpr float K = T == KVQ_Q4_0 ? 8.0f : 16.0f;
+            constexpr int cmax = T == KVQ_Q4_0 ? 15 : 31;
+            float best = x[0], ba = fabsf(x[0]);
+#pragma unroll
+            for (int i = 1; i < kBlock; ++i) {
+                const float a = fabsf(x[i]);
+                if (a > ba) {
+                    ba = a;
+                    best = x[i];
+                }
+            }
+            d = __fdiv_rn(best, -K);
+            const float id = d != 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < kBlock; ++i) {
+                const int t = static_cast<int>(__fadd_rn(__fmul_rn(x[i], id), K + 0.5f));  // truncation
+                c[i] = t < cmax ? t : cmax;
+            }
+        } else {
+            // lo = min, hi = max, d = (hi - lo) / L, codes min(L, trunc((x - lo) / d + 1/2))
+            constexpr int L = T == KVQ_Q4_1 ? 15 : 31;
+            float hi = x[0];
+            lo = x[0];
+#pragma unroll
+            for (int i = 1; i < kBlock; ++i) {
+                lo = fminf(lo, x[i]);
+                hi = fmaxf(hi, x[i]);
+            }
+            d = __fdiv_rn(__fsub_rn(hi, lo), static_cast<float>(L));
+            const float id = d != 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < kBlock; ++i) {
+                const int t = static_cast<int>(__fadd_rn(__fmul_rn(__fsub_rn(x[i], lo), id), 0.5f));
+                c[i] = t < L ? t : L;
+            }
+        }
+        // low 4 bits in the nibble bytes (value i in the low nibble, i + 16 in the high one);
+        // for 5-bit types the fifth bits in the plane after the nibbles (bit positions as in
+        // quantize_store_vals; other rows' bits of a word are kept)
+        uint32_t *hb_chunk = reinterpret_cast<uint32_t *>(codes + kNibbleBytes + (b >> 1) * 128);
+        if constexpr (!IS_V) {
+#pragma unroll
+            for (int g4 = 0; g4 < 4; ++g4) {
+                uint32_t w = 0, mask = 0, bits = 0;
+                const int wi = 2 * (b & 1) + st;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int lo_c = c[4 * g4 + e], hi_c = c[4 * g4 + 16 + e];
+                    w |= (uint32_t(lo_c & 15) | (uint32_t(hi_c & 15) << 4)) << (8 * e);
+                    mask |= (1u << (8 * e + 4 + wi)) | (1u << (8 * e + wi));
+                    bits |= (uint32_t(lo_c >> 4) << (8 * e + 4 + wi)) | (uint32_t(hi_c >> 4) << (8 * e + wi));
+                }
+                *reinterpret_cast<uint32_t *>(codes + (b >> 1) * 512 + (4 * n + g4) * 16 + (2 * (b & 1) + st) * 4) = w;
+                if constexpr (has_fifth_bit(T)) {
+                    atomicAnd(hb_chunk + (4 * n + g4), ~mask);
+                    atomicOr(hb_chunk + (4 * n + g4), bits);
+                }
+            }
+        } else {
+            const int vb = vword_byte(pos);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int n2 = i >> 1, qq = i & 1;
+                codes[(b >> 1) * 512 + (4 * n2 + j) * 16 + (2 * (b & 1) + qq) * 4 + vb] =
+                    static_cast<uint8_t>(uint32_t(c[i] & 15) | (uint32_t(c[i + 16] & 15) << 4));
+                if constexpr (has_fifth_bit(T)) {
+                    const int wi = 2 * (b & 1) + qq;
+                    const uint32_t mask = (1u << (8 * vb + 4 + wi)) | (1u << (8 * vb + wi));
+                    const uint32_t bits = (uint32_t(c[i] >> 4) << (8 * vb + 4 + wi)) | (uint32_t(c[i + 16] >> 4) << (8 * vb + wi));
+                    atomicAnd(hb_chunk + (4 * n2 + j), ~mask);
+                    atomicOr(hb_chunk + (4 * n2 + j), bits);
+                }
+            }
+        }
+        *reinterpret_cast<__half *>(scales + j * 32 + b * 8 + pos * 2) = __float2half_rn(d);
+        if constexpr (has_min(T)) *reinterpret_cast<__half *>(scales + kScaleTile + j * 32 + b * 8 + pos * 2) = __float2half_rn(lo);
+        return;
+    }
+}
+
 // The inverse of quantize_store_vals<KVQ_F16, IS_V>: values 4l..4l+3 of row kt of an f16
 // tile slice, widened to fp32 (exact).
 template <bool IS_V>
