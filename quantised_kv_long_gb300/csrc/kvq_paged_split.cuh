@@ -60,7 +60,7 @@ struct SplitCfg {
     static constexpr int SMEM = OFF_BAR + WARPS * SLOTS * 8;
     static constexpr int D = T::D;
     static_assert(SLOTS >= 2, "a step in flight while one is read");
-    static_assert(SMEM + 1536 <= 232448, "shared memory of one CTA");
+    static_assert(SMEM + 2560 <= 232448, "shared memory of one CTA");
     static_assert(WARPS * (kRows * D + 2 * kRows) * 4 <= RING, "merge buffer in the ring");
 };
 
@@ -104,6 +104,12 @@ __device__ __forceinline__ uint32_t code8_13(uint32_t w) { return byte_perm0<0xB
 constexpr uint32_t kLowNib = 0x000f000fu, kHighNib = 0x00f000f0u;
 constexpr float kUnit24 = 16777216.0f, kUnit20 = 1048576.0f;
 
+// d = A B + C with C = (c0, c1) in every row
+__device__ __forceinline__ void mma_16816_c(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};\n"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) { return h2_as_u32(__floats2half2_rn(a, b)); }
 
 // The query rows of a unit as B operands, and what belongs to the rows this lane's accumulator
@@ -112,7 +118,7 @@ template <int KT, int NS, bool QLO>
 struct QueryFrags {
     uint32_t hi[NS * 8][2], lo[QLO ? NS * 8 : 1][2];
     float corr[KT == KVQ_Q4_0 ? NS * 4 : 1][2];  // -8 times the sum of q over each block, in accumulator units
-    float scale[2];                              // S to log2 units
+    float scale[2];                              // raw scores (accumulator units) to log2 units, >= 0
 };
 
 template <int KT, int NS, bool QLO, int DT>
@@ -131,8 +137,9 @@ __device__ __forceinline__ void load_queries(QueryFrags<KT, NS, QLO> &f, const t
     const int ex = static_cast<int>(__float_as_uint(top) >> 23);
     int k = (ex == 0 && top == 0.f) || ex == 255 ? 0 : 10 - (ex - 127);
     k = max(-120, min(120, k));
-    const float up = __int_as_float((127 + k) << 23), down = __int_as_float((127 - k) << 23);
-    const float rs = scale * kSplitLog2e * down * (KT == KVQ_F16 ? 1.f : (KT == KVQ_Q4_0 ? kUnit20 : kUnit24));
+    // a negative scale goes to the query, so that the largest raw score of a row is its largest score
+    const float up = __int_as_float(((127 + k) << 23) | (scale < 0.f ? 0x80000000 : 0)), down = __int_as_float((127 - k) << 23);
+    const float rs = fabsf(scale) * kSplitLog2e * down * (KT == KVQ_F16 ? 1.f : (KT == KVQ_Q4_0 ? kUnit20 : kUnit24));
     float sum[NS * 4];
 #pragma unroll
     for (int c = 0; c < NS * 8; ++c) {
@@ -161,11 +168,12 @@ __device__ __forceinline__ void load_queries(QueryFrags<KT, NS, QLO> &f, const t
             f.corr[b][1] = __shfl_sync(0xffffffffu, sum[b], 8 * j + 4);
         }
     }
-    f.scale[0] = __shfl_sync(0xffffffffu, rs, 8 * j);
-    f.scale[1] = __shfl_sync(0xffffffffu, rs, 8 * j + 4);
+    // never 0, so that a masked score stays -inf
+    f.scale[0] = fmaxf(__shfl_sync(0xffffffffu, rs, 8 * j), 1e-36f);
+    f.scale[1] = fmaxf(__shfl_sync(0xffffffffu, rs, 8 * j + 4), 1e-36f);
 }
 
-// Scores of one tile: s[0], s[1] = key g with rows 2j, 2j + 1; s[2], s[3] = key g + 8 (g = lane / 4).
+// Raw scores of one tile: s[0], s[1] = key g with rows 2j, 2j + 1; s[2], s[3] = key g + 8 (g = lane / 4).
 template <int KT, int NS, bool QLO>
 __device__ __forceinline__ void tile_s(const uint8_t *kc, const uint8_t *ks, const QueryFrags<KT, NS, QLO> &f, float (&s)[4]) {
     const int lane = threadIdx.x & 31, g = lane >> 2;
@@ -188,7 +196,7 @@ __device__ __forceinline__ void tile_s(const uint8_t *kc, const uint8_t *ks, con
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = (acc[0][i] + acc[1][i]) * f.scale[i & 1];
+        for (int i = 0; i < 4; ++i) s[i] = acc[0][i] + acc[1][i];
     } else {
         s[0] = s[1] = s[2] = s[3] = 0.f;
         // key g is member g % 2 of the pairs of lane group g / 2, key g + 8 member 2 + g % 2
@@ -215,9 +223,7 @@ __device__ __forceinline__ void tile_s(const uint8_t *kc, const uint8_t *ks, con
                     a0[0] = u & kLowNib, a0[1] = w & kLowNib, a0[2] = u8 & kLowNib, a0[3] = w8 & kLowNib;
                     a1[0] = u & kHighNib, a1[1] = w & kHighNib, a1[2] = u8 & kHighNib, a1[3] = w8 & kHighNib;
                     const int bi = sl * 4 + b;
-                    acc[0] = acc[2] = f.corr[bi][0];
-                    acc[1] = acc[3] = f.corr[bi][1];
-                    mma_16816(acc, a0, f.hi[c][0], f.hi[c][1]);
+                    mma_16816_c(acc, a0, f.hi[c][0], f.hi[c][1], f.corr[bi][0], f.corr[bi][1]);
                 }
                 mma_16816(acc, a1, f.hi[c + 1][0], f.hi[c + 1][1]);
                 if constexpr (QLO) {
@@ -234,23 +240,23 @@ __device__ __forceinline__ void tile_s(const uint8_t *kc, const uint8_t *ks, con
                 s[3] = fmaf(d1, acc[3], s[3]);
             }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] *= f.scale[i & 1];
     }
 }
 
-// Whether this lane's rows of a tile (masks mab, mcd as in tile_o) have a value scale of 2 or more:
-// bit 14 of a half, inf and NaN included.
+// Whether rows [0, valid) of a tile have a value scale of 2 or more (bit 14 of a half; inf and NaN included):
+// each lane looks at one word, keys 2j, 2j + 1 (+ 8 in odd words) of lane group j = lane / 8.
 template <int NS>
-__device__ __forceinline__ bool big_scales(const uint8_t *vs, uint32_t mab, uint32_t mcd) {
-    const int j = threadIdx.x & 3;
+__device__ __forceinline__ bool big_scales(const uint8_t *vs, int valid) {
+    const int lane = threadIdx.x & 31;
     uint32_t e = 0;
 #pragma unroll
-    for (int sl = 0; sl < NS; ++sl) {
-        const uint4 a = lds128(vs + sl * kScaleTile + j * 32), b = lds128(vs + sl * kScaleTile + j * 32 + 16);
-        e |= ((a.x | a.z | b.x | b.z) & mab) | ((a.y | a.w | b.y | b.w) & mcd);
+    for (int sl = 0; sl < NS; ++sl) e |= *reinterpret_cast<const uint32_t *>(vs + sl * kScaleTile + lane * 4);
+    e &= 0x40004000u;
+    if (valid < kTileRows) {
+        const int k = 2 * (lane >> 3) + 8 * (lane & 1);
+        e &= k >= valid ? 0u : (k + 1 >= valid ? 0x0000ffffu : 0xffffffffu);
     }
-    return (e & 0x40004000u) != 0;
+    return e != 0;
 }
 
 // O^T += V^T P^T for one tile.  ph / pl: weights of keys (2j, 2j + 1) and (2j + 8, 2j + 9) of row g;
@@ -349,7 +355,7 @@ __device__ __forceinline__ void walk_seq(Walk &w, const PagedAttnParams &p, int 
 }
 // position at step x of all steps; pre[b] <= x < pre[n_seqs]
 template <int TPS>
-__device__ __forceinline__ void walk_to(Walk &w, const PagedAttnParams &p, const int *pre, int x) {
+__device__ __noinline__ Walk walk_to(const PagedAttnParams &p, const int *pre, int x) {
     int lo = 0, hi = p.v.n_seqs;  // last b with pre[b] <= x (it has steps, for pre[b + 1] > x)
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -358,20 +364,23 @@ __device__ __forceinline__ void walk_to(Walk &w, const PagedAttnParams &p, const
         else
             hi = mid;
     }
+    Walk w;
     walk_seq<TPS>(w, p, lo);
     const int r = x - pre[lo];
     w.unit = r / w.steps;
     w.t = r - w.unit * w.steps;
+    return w;
 }
 // the first step of the next unit (a step follows: the caller counts)
 template <int TPS>
-__device__ __forceinline__ void walk_next_unit(Walk &w, const PagedAttnParams &p, const int *pre) {
+__device__ __noinline__ Walk walk_next_unit(Walk w, const PagedAttnParams &p, const int *pre) {
     w.t = 0;
-    if (++w.unit < w.units) return;
+    if (++w.unit < w.units) return w;
     int b = w.b + 1;
     while (pre[b + 1] == pre[b]) ++b;
     walk_seq<TPS>(w, p, b);
     w.unit = 0;
+    return w;
 }
 
 // Row r of a unit (row group qg of KV head h of sequence b): its output row, or -1.
@@ -399,6 +408,9 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
     __shared__ int s_scan[32];
     __shared__ int s_unit[C::WARPS], s_b[C::WARPS];  // the unit a warp's accumulators hold at the end (-1: none)
     __shared__ float s_ml[C::WARPS][2 * kRows];
+    // where a warp's issuing and reading sides stand: kept out of the registers of the loop, which needs them
+    // once per page and once per unit
+    __shared__ Walk s_walk[C::WARPS][2];
     int *pre = reinterpret_cast<int *>(smem + C::OFF_PRE);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, j = lane & 3;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR) + warp * C::SLOTS;
@@ -447,13 +459,13 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
 
     float o[NS * 8][4], corr[4], m_run[2], l[2], bias = kBias;
     if (lane == 0) s_unit[warp] = -1;
-    QueryFrags<KT, NS, C::QLO> f;
-    UnitRows rows{};
-    int seg0 = x0;  // first step of the segment in hand
-    Walk cur{};
+    // output rows of a unit
+    auto rows_of = [&](const Walk &w) {
+        const int h = w.unit / w.groups;
+        return unit_rows(p, split_seq(p, w.b), h, w.unit - h * w.groups);
+    };
 
-    // a finished segment [seg0, end) of the unit in hand, in its registers: l summed over the keys' lanes,
-    // o in real units
+    // a finished segment in its registers: l summed over the keys' lanes, o in real units
     auto finish = [&]() {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -478,7 +490,7 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
         }
     };
     // the unit's output rows, from a segment that is all of it
-    auto write_out = [&]() {
+    auto write_out = [&](const UnitRows &rows) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const long long row = rows.out_row(2 * j + i);
@@ -505,95 +517,129 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
         }
     };
 
+    Walk *const w_iss = &s_walk[warp][0], *const w_cur = &s_walk[warp][1];
     if (x0 < x1) {
-        uint8_t *ring = smem + warp * (C::SLOTS * C::STEP);
-        // ---- the issuing side runs SLOTS steps ahead ----
-        Walk iss;
-        walk_to<TPS>(iss, p, pre, x0);
-        cur = iss;
-        int ix = x0;                // its step
-        int pg = 0, tip = 0;        // table entry and tile in page of its first tile
-        int page[TPS];              // page numbers of its tiles, loaded one step ahead
-        unsigned held = 0;          // bit slot * TPS + i: tile i of the slot's step was copied
-        auto locate = [&]() {
-            const int t0 = iss.t * TPS;
-            pg = t0 / v.page_tiles;
-            tip = t0 - pg * v.page_tiles;
+        uint8_t *const ring = smem + warp * (C::SLOTS * C::STEP);
+        constexpr unsigned kAll = (1u << TPS) - 1u;
+        {
+            const Walk w = walk_to<TPS>(p, pre, x0);
+            if (lane == 0) *w_iss = *w_cur = w;
+            __syncwarp();
+        }
+        // ---- the issuing side runs SLOTS steps ahead.  Steps whose tiles follow one another in a page form a
+        // run, found once: within it a step is one copy from `src`.  A lane holds one entry of the unit's
+        // block table (entries tab0 .. tab0 + 31), the next 32 are on their way. ----
+        int to_issue = x1 - x0, run = 0;
+        const uint8_t *src = nullptr;
+        unsigned held = 0;  // bit slot * TPS + i: tile i of the slot's step was copied
+        int tab = -1, tab_next = -1, tab0 = 0;
+        auto load_tab = [&](const Walk &w, int e0) {
+            const int entries = (w.tiles + v.page_tiles - 1) / v.page_tiles;
+            return e0 + lane < entries ? __ldg(v.table + static_cast<size_t>(w.b) * v.stride + e0 + lane) : -1;
         };
-        auto look_up = [&]() {
-            const int32_t *row = v.table + static_cast<size_t>(iss.b) * v.stride;
-#pragma unroll
-            for (int i = 0; i < TPS; ++i) {
-                int e = pg, q = tip + i;
-                while (q >= v.page_tiles) q -= v.page_tiles, ++e;
-                page[i] = iss.t * TPS + i < iss.tiles ? __ldg(row + e) : -1;
-            }
+        auto enter_unit = [&](const Walk &w) {
+            tab0 = w.t * TPS / v.page_tiles;
+            tab = load_tab(w, tab0);
+            tab_next = load_tab(w, tab0 + 32);
         };
-        auto issue = [&](int slot) {  // the copies of step ix, and on to the next
-            const int h = iss.unit / iss.groups;
+        enter_unit(*w_iss);
+        auto copy = [&](uint8_t *dst, const uint8_t *from, int bytes, uint64_t *bar) {
+            if (lane == 0) bulk_g2s(dst, from, bytes, bar);
+        };
+        auto issue = [&](int slot) {  // the next step into a slot
             uint8_t *dst = ring + slot * C::STEP;
-            bool in[TPS];
-            int n = 0;
-#pragma unroll
-            for (int i = 0; i < TPS; ++i) {
-                in[i] = page[i] >= 0 && page[i] < v.n_pages;
-                n += in[i] ? 1 : 0;
-                if (!in[i] && iss.t * TPS + i < iss.tiles && lane == 0) paged_error(v);
-                held = (held & ~(1u << (slot * TPS + i))) | (in[i] ? 1u << (slot * TPS + i) : 0u);
-            }
-            if (lane == 0) {
-                const size_t hp = static_cast<size_t>(v.page_tiles) * T::BYTES;
-                auto src = [&](int i) {
-                    int q = tip + i;
-                    while (q >= v.page_tiles) q -= v.page_tiles;
-                    return v.pool + (static_cast<size_t>(page[i]) * v.Hkv + h) * hp + static_cast<size_t>(q) * T::BYTES;
+            if (run == 0) {
+                Walk w = *w_iss;
+                if (w.t == w.steps) {
+                    w = walk_next_unit<TPS>(w, p, pre);
+                    enter_unit(w);
+                }
+                const int h = w.unit / w.groups, t0 = w.t * TPS;
+                auto entry = [&](int e) {  // e grows by at most one per call
+                    if (e - tab0 >= 32) {
+                        tab = tab_next;
+                        tab0 += 32;
+                        tab_next = load_tab(w, tab0 + 32);
+                    }
+                    return __shfl_sync(0xffffffffu, tab, e - tab0);
                 };
-                mbar_arrive_expect_tx(full + slot, static_cast<uint32_t>(n * T::BYTES));
-                if (TPS == 2 && in[0] && in[TPS - 1] && tip + 1 < v.page_tiles) {
-                    bulk_g2s(dst, src(0), 2 * T::BYTES, full + slot);
+                auto record = [&](int page, int q) {
+                    return v.pool + ((static_cast<size_t>(page) * v.Hkv + h) * v.page_tiles + q) * T::BYTES;
+                };
+                const int e = t0 / v.page_tiles, q = t0 - e * v.page_tiles;
+                const int page = entry(e);
+                const bool in = page >= 0 && page < v.n_pages;
+                const int whole = min(v.page_tiles - q, w.tiles - t0) / TPS;  // steps of this page from here
+                int done = 1;
+                if (in && whole > 0) {
+                    src = record(page, q);
+                    run = done = min(whole, to_issue);
                 } else {
+                    // a step that crosses a page, ends the sequence or has no page: tile by tile
+                    bool ok[TPS];
+                    const uint8_t *from[TPS];
+                    int n = 0;
+#pragma unroll
+                    for (int i = 0; i < TPS; ++i) {
+                        int ei = e, qi = q + i;
+                        if (qi >= v.page_tiles) qi -= v.page_tiles, ++ei;
+                        const bool live = t0 + i < w.tiles;
+                        const int pi = i == 0 ? page : (live ? entry(ei) : -1);
+                        ok[i] = live && pi >= 0 && pi < v.n_pages;
+                        from[i] = ok[i] ? record(pi, qi) : nullptr;
+                        if (live && !ok[i] && lane == 0) paged_error(v);
+                        n += ok[i] ? 1 : 0;
+                        const unsigned bit = 1u << (slot * TPS + i);
+                        held = ok[i] ? held | bit : held & ~bit;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(full + slot, static_cast<uint32_t>(n * T::BYTES));
+                    __syncwarp();
 #pragma unroll
                     for (int i = 0; i < TPS; ++i)
-                        if (in[i]) bulk_g2s(dst + i * T::BYTES, src(i), T::BYTES, full + slot);
+                        if (ok[i]) copy(dst + i * T::BYTES, from[i], T::BYTES, full + slot);
                 }
+                __syncwarp();
+                if (lane == 0) {
+                    w.t += done;
+                    *w_iss = w;
+                }
+                __syncwarp();
             }
-            if (++ix >= x1) return;
-            if (++iss.t < iss.steps) {
-                tip += TPS;
-                while (tip >= v.page_tiles) tip -= v.page_tiles, ++pg;
-            } else {
-                walk_next_unit<TPS>(iss, p, pre);
-                pg = tip = 0;
+            if (run > 0) {
+                if (lane == 0) mbar_arrive_expect_tx(full + slot, C::STEP);
+                copy(dst, src, C::STEP, full + slot);
+                src += C::STEP;
+                --run;
+                held |= kAll << (slot * TPS);
             }
-            look_up();
+            --to_issue;
         };
-        locate();
-        look_up();
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < C::SLOTS; ++i)
-            if (ix < x1) issue(i);
+            if (to_issue > 0) issue(i);
 
         // ---- the reading side ----
-        int lim[2] = {0, 0}, lim_min = 0, len = 0;
-        bool fresh = true;
+        QueryFrags<KT, NS, C::QLO> f;
+        int lim[2] = {0, 0}, lim_min = 0, len = 0, key0 = 0, unit_left = 0, left = x1 - x0;
+        bool first = true;  // the segment in hand is the span's first
         int slot = 0;
         unsigned phase = 0;
-        for (int x = x0; x < x1; ++x) {
-            if (fresh) {  // a new unit: its queries, empty accumulators
-                fresh = false;
-                seg0 = x;
-                const PagedSeq s = split_seq(p, cur.b);
-                const int h = cur.unit / cur.groups, qg = cur.unit - h * cur.groups;
-                rows = unit_rows(p, s, h, qg);
+        while (true) {
+            if (unit_left == 0) {  // a unit: its queries, empty accumulators
+                const Walk w = *w_cur;
+                const UnitRows rows = rows_of(w);
+                const PagedSeq s = split_seq(p, w.b);
                 len = s.len;
                 lim_min = s.len - s.n;  // the first token's position
 #pragma unroll
                 for (int i = 0; i < 2; ++i) lim[i] = lim_min + (rows.r0 + 2 * j + i) / p.G;
+                key0 = w.t * TPS * kTileRows;
+                unit_left = w.steps - w.t;
                 const long long row = rows.out_row(g);  // token * Hq + head
-                const X *src = nullptr;
+                const X *qr = nullptr;
                 if (row >= 0)
-                    src = static_cast<const X *>(p.q) + (row / p.Hq) * p.q_stride + static_cast<size_t>(row % p.Hq) * D;
-                load_queries<KT, NS, C::QLO, DT>(f, src, p.scale);
+                    qr = static_cast<const X *>(p.q) + (row / p.Hq) * p.q_stride + static_cast<size_t>(row % p.Hq) * D;
+                load_queries<KT, NS, C::QLO, DT>(f, qr, p.scale);
 #pragma unroll
                 for (int t = 0; t < NS * 8; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
                 corr[0] = corr[1] = corr[2] = corr[3] = 0.f;
@@ -606,30 +652,32 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
                 // gave up: the outputs of the call are undefined and the error word says so.  Copies in
                 // flight land before the memory is used again.
                 if (lane == 0) atomicOr(v.err, KVQ_DEVERR_TIMEOUT);
-                for (; x < ix; ++x) {
+                for (int i = left - to_issue; i > 0; --i) {
                     (void)paged_wait(full + slot, phase);
                     if (++slot == C::SLOTS) slot = 0, phase ^= 1u;
                 }
                 break;
             }
-            const unsigned got = held >> (slot * TPS);
+            const unsigned got = (held >> (slot * TPS)) & kAll;
             float s[TPS][4];
 #pragma unroll
-            for (int i = 0; i < TPS; ++i) {
+            for (int i = 0; i < TPS; ++i)
                 tile_s<KT, NS, C::QLO>(st + i * T::BYTES, st + i * T::BYTES + T::OFF_KS, f, s[i]);
-            }
             // keys behind a row's own position, past the end or in no page
-            const int key0 = cur.t * TPS * kTileRows;
-            const unsigned all = (1u << TPS) - 1u;
-            const bool cut = key0 + TPS * kTileRows - 1 > lim_min || (got & all) != all;
+            const bool cut = key0 + TPS * kTileRows - 1 > lim_min || got != kAll;
+            int valid[TPS];  // rows of each tile in use
+#pragma unroll
+            for (int i = 0; i < TPS; ++i) valid[i] = kTileRows;
             if (cut) {
 #pragma unroll
-                for (int i = 0; i < TPS; ++i)
+                for (int i = 0; i < TPS; ++i) {
+                    valid[i] = ((got >> i) & 1u) ? len - key0 - i * kTileRows : 0;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int key = key0 + i * kTileRows + g + (e >> 1) * 8;
-                        if (key > lim[e & 1] || key >= len || !((got >> i) & 1u)) s[i][e] = -CUDART_INF_F;
+                        const int key = i * kTileRows + g + (e >> 1) * 8;
+                        if (key0 + key > lim[e & 1] || key - i * kTileRows >= valid[i]) s[i][e] = -CUDART_INF_F;
                     }
+                }
             }
             // ---- running maximum: moved only when a score passes it by kDrift ----
             float mx[2] = {s[0][0], s[0][1]};
@@ -637,28 +685,20 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
             for (int i = 0; i < TPS; ++i)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) mx[e] = fmaxf(mx[e], fmaxf(s[i][e], s[i][2 + e]));
-            // rows of each tile in use, as masks of this lane's key pairs
-            uint32_t mab[TPS], mcd[TPS];
-#pragma unroll
-            for (int i = 0; i < TPS; ++i) {
-                mab[i] = mcd[i] = 0xffffffffu;
-                if (cut) {
-                    const int valid = ((got >> i) & 1u) ? len - key0 - i * kTileRows : 0;
-                    auto mask = [&](int k) { return k + 1 < valid ? 0xffffffffu : (k < valid ? 0x0000ffffu : 0u); };
-                    mab[i] = mask(2 * j);
-                    mcd[i] = mask(2 * j + 8);
-                }
-            }
-            bool lower = false;
+            mx[0] *= f.scale[0];
+            mx[1] *= f.scale[1];
+            bool big = false;
             if constexpr (VT != KVQ_F16) {
-                bool big = false;
 #pragma unroll
-                for (int i = 0; i < TPS; ++i) big = big_scales<NS>(st + i * T::BYTES + T::OFF_VS, mab[i], mcd[i]) || big;
-                lower = bias == kBias && __any_sync(0xffffffffu, big);
+                for (int i = 0; i < TPS; ++i) big = big_scales<NS>(st + i * T::BYTES + T::OFF_VS, valid[i]) || big;
+                big = big && bias == kBias;
             }
-            if (__any_sync(0xffffffffu, mx[0] > m_run[0] + kDrift || mx[1] > m_run[1] + kDrift) || lower) {
-                const float shift = lower ? kBiasBig - kBias : 0.f;
-                if (lower) bias = kBiasBig;
+            if (__any_sync(0xffffffffu, mx[0] > m_run[0] + kDrift || mx[1] > m_run[1] + kDrift || big)) {
+                float shift = 0.f;
+                if (VT != KVQ_F16 && __any_sync(0xffffffffu, big)) {
+                    shift = kBiasBig - kBias;
+                    bias = kBiasBig;
+                }
                 float a[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -682,12 +722,12 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
                     corr[1] *= a[1];
                 }
             }
-            const float ms[2] = {m_run[0] == -CUDART_INF_F ? 0.f : m_run[0] - bias, m_run[1] == -CUDART_INF_F ? 0.f : m_run[1] - bias};
+            const float ms[2] = {m_run[0] == -CUDART_INF_F ? 0.f : bias - m_run[0], m_run[1] == -CUDART_INF_F ? 0.f : bias - m_run[1]};
 #pragma unroll
             for (int i = 0; i < TPS; ++i) {
                 float w[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = fast_ex2(s[i][e] - ms[e & 1]);
+                for (int e = 0; e < 4; ++e) w[e] = fast_ex2(fmaf(s[i][e], f.scale[e & 1], ms[e & 1]));
                 l[0] += w[0] + w[2];
                 l[1] += w[1] + w[3];
                 uint32_t ph[2] = {pack_half2(w[0], w[1]), pack_half2(w[2], w[3])}, pl[2] = {0u, 0u};
@@ -699,31 +739,40 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
                 ph[0] = transpose8x8(ph[0]);
                 ph[1] = transpose8x8(ph[1]);
                 const uint8_t *tv = st + i * T::BYTES + T::OFF_V, *tvs = st + i * T::BYTES + T::OFF_VS;
-                if (cut)
-                    tile_o<VT, NS, C::PLO, true>(tv, tvs, ph, pl, mab[i], mcd[i], o, corr);
-                else
-                    tile_o<VT, NS, C::PLO, false>(tv, tvs, ph, pl, mab[i], mcd[i], o, corr);
+                if (cut) {
+                    auto mask = [&](int k) { return k + 1 < valid[i] ? 0xffffffffu : (k < valid[i] ? 0x0000ffffu : 0u); };
+                    tile_o<VT, NS, C::PLO, true>(tv, tvs, ph, pl, mask(2 * j), mask(2 * j + 8), o, corr);
+                } else {
+                    tile_o<VT, NS, C::PLO, false>(tv, tvs, ph, pl, 0u, 0u, o, corr);
+                }
             }
             __syncwarp();  // the slot has been read
-            if (ix < x1) issue(slot);
+            if (to_issue > 0) issue(slot);
             if (++slot == C::SLOTS) {
                 slot = 0;
                 phase ^= 1u;
             }
-            if (++cur.t == cur.steps && x + 1 < x1) {  // the unit ends inside this warp's span
+            key0 += TPS * kTileRows;
+            --unit_left;
+            if (--left == 0) break;
+            if (unit_left == 0) {  // the unit ends inside this warp's span
+                Walk w = *w_cur;
                 finish();
-                if (seg0 > x0 || cur.steps == x + 1 - seg0)
-                    write_out();
+                if (!first || w.t == 0)
+                    write_out(rows_of(w));
                 else
                     write_piece(gw * 2 + 1);
-                walk_next_unit<TPS>(cur, p, pre);
-                fresh = true;
+                w = walk_next_unit<TPS>(w, p, pre);
+                __syncwarp();
+                if (lane == 0) *w_cur = w;
+                __syncwarp();
+                first = false;
             }
         }
         finish();
         if (lane == 0) {
-            s_unit[warp] = cur.unit;
-            s_b[warp] = cur.b;
+            s_unit[warp] = w_cur->unit;
+            s_b[warp] = w_cur->b;
         }
     }
     // ---- the warps of this CTA whose last segments are of one unit merge ----
@@ -736,12 +785,14 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
         while (same(last + 1)) ++last;
     }
     // the group holds steps [its first warp's segment start, the end of the unit or of its spans)
-    const int u0 = unit >= 0 ? pre[ub] + unit * cur.steps : 0;
+    const int steps = unit >= 0 ? w_cur->steps : 0, u0 = unit >= 0 ? pre[ub] + unit * steps : 0;
+    UnitRows rows{};
+    if (unit >= 0) rows = rows_of(*w_cur);
     const int g0 = max(u0, (blockIdx.x * C::WARPS + first) * span), g1 = min(total, (static_cast<int>(blockIdx.x) * C::WARPS + last + 1) * span);
-    const bool whole = unit >= 0 && g0 == u0 && g1 >= u0 + cur.steps;
+    const bool whole = unit >= 0 && g0 == u0 && g1 >= u0 + steps;
     if (unit >= 0 && first == last) {
         if (whole)
-            write_out();
+            write_out(rows);
         else
             write_piece((blockIdx.x * C::WARPS + warp) * 2);
     }
