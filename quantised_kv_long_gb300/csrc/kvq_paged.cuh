@@ -93,6 +93,10 @@ __device__ __forceinline__ bool paged_wait(uint64_t *bar, uint32_t parity) {
     }
 }
 
+// At the head of a rarely taken branch: keeps the compiler from turning the branch into selects that every
+// pass would execute.
+__device__ __forceinline__ void keep_branch() { asm volatile("" ::: "memory"); }
+
 // ---- activations: fp32, f16, bf16 ----
 template <int DT>
 struct Act;

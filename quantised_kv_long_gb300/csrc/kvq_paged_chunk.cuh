@@ -530,6 +530,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
                     uint4 w = *reinterpret_cast<const uint4 *>(sc + i * T::BYTES + in * 16);
                     const int use = rows_of(len, t, got, i), ka = 2 * ((in & 7) >> 1);
                     if (use < kTileRows) {
+                        keep_branch();
                         auto cut = [&](uint32_t x, int r) { return r >= use ? 0u : (r + 1 >= use ? (x & 0xffffu) : x); };
                         w = make_uint4(cut(w.x, ka), cut(w.y, ka + 8), cut(w.z, ka), cut(w.w, ka + 8));
                     }
@@ -775,6 +776,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
                         // keys behind the row's position (and so past the end) and those in no page
                         const int key0 = (c0 + c) * NK;
                         if (__any_sync(0xffffffffu, rv && key0 + NK - 1 > lim) || got != (1 << C::TILES) - 1) {
+                            keep_branch();
 #pragma unroll
                             for (int k = 0; k < NK; ++k)
                                 if (key0 + k > lim || !((got >> (k / kTileRows)) & 1)) s[k] = -CUDART_INF_F;

@@ -32,7 +32,7 @@
 namespace kvq {
 namespace {
 
-constexpr int kSplitMaxSeqs = 1024;  // sequences of one launch (their prefix sums sit in shared memory)
+constexpr int kSplitMaxSeqs = 512;  // sequences of one launch (their prefix sums and shapes sit in shared memory)
 constexpr int kRows = 8;             // query rows of a unit: the columns of the MMA
 constexpr float kDrift = 4.0f;       // the running maximum is moved when a score passes it by this (log2)
 // Weights are 2^(s - m + bias).  bias 10 puts the largest weight at 2^10 .. 2^14, so that weights of
@@ -47,16 +47,17 @@ struct SplitCfg {
     static constexpr bool QLO = DT == KVQ_DT_F32;   // queries as hi + lo
     static constexpr bool PLO = DT != KVQ_DT_BF16;  // weights as hi + lo
     // tiles per step (32 keys share one softmax step where the ring allows), warps, ring slots
-    static constexpr int TPS = (NS == 1 && T::BYTES <= 2304) ? 2 : 1;
-    static constexpr int WARPS = NS == 1 ? (KT == KVQ_F16 ? 8 : 16) : (KT == KVQ_F16 ? 4 : (QLO ? 8 : 12));
+    static constexpr int TPS = NS == 1 && KT != KVQ_F16 && !QLO ? 2 : 1;
+    static constexpr int WARPS = NS == 1 ? (KT == KVQ_F16 ? 8 : (QLO ? 16 : 12)) : (KT == KVQ_F16 ? 4 : (QLO ? 8 : 12));
     static constexpr int STEP = TPS * T::BYTES;
-    static constexpr int RING_MAX = 222000;
+    static constexpr int RING_MAX = 223000;
     static constexpr int SLOTS_RAW = RING_MAX / (WARPS * STEP);
     static constexpr int SLOTS = SLOTS_RAW > 6 ? 6 : SLOTS_RAW;
     static constexpr int RING = WARPS * SLOTS * STEP;
     static constexpr int THREADS = WARPS * 32;
-    static constexpr int OFF_PRE = RING;                                 // int [kSplitMaxSeqs + 1]
-    static constexpr int OFF_BAR = OFF_PRE + (kSplitMaxSeqs + 2) * 4;    // full barriers [WARPS][SLOTS]
+    static constexpr int OFF_PRE = RING;                                    // int [kSplitMaxSeqs + 1]
+    static constexpr int OFF_SHAPE = OFF_PRE + (kSplitMaxSeqs + 2) * 4;     // int2 [kSplitMaxSeqs]: tiles, row groups
+    static constexpr int OFF_BAR = OFF_SHAPE + kSplitMaxSeqs * 8;           // full barriers [WARPS][SLOTS]
     static constexpr int SMEM = OFF_BAR + WARPS * SLOTS * 8;
     static constexpr int D = T::D;
     static_assert(SLOTS >= 2, "a step in flight while one is read");
@@ -140,35 +141,39 @@ __device__ __forceinline__ void load_queries(QueryFrags<KT, NS, QLO> &f, const t
     // a negative scale goes to the query, so that the largest raw score of a row is its largest score
     const float up = __int_as_float(((127 + k) << 23) | (scale < 0.f ? 0x80000000 : 0)), down = __int_as_float((127 - k) << 23);
     const float rs = fabsf(scale) * kSplitLog2e * down * (KT == KVQ_F16 ? 1.f : (KT == KVQ_Q4_0 ? kUnit20 : kUnit24));
-    float sum[NS * 4];
 #pragma unroll
     for (int c = 0; c < NS * 8; ++c) {
         // low nibbles count 1 and high nibbles 16 of the accumulator's unit
-        const float u = (KT == KVQ_Q4_0 && (c & 1) == 0) ? 16.f : 1.f;
-        const float a = x[c].x * up, b = x[c].y * up, e = x[c].z * up, d = x[c].w * up;
-        if ((c & 1) == 0) sum[c >> 1] = 0.f;
-        sum[c >> 1] += (a + b) + (e + d);
+        const float u = (KT == KVQ_Q4_0 && (c & 1) == 0) ? up * 16.f : up;
+        const float a = x[c].x * u, b = x[c].y * u, e = x[c].z * u, d = x[c].w * u;
         // k = 2j, 2j + 1 of the MMA are values 0, 2 of the four and 2j + 8, 2j + 9 values 1, 3 (the
         // order in which the key codes' bytes come out of a word)
-        f.hi[c][0] = pack_half2(a * u, e * u);
-        f.hi[c][1] = pack_half2(b * u, d * u);
+        f.hi[c][0] = pack_half2(a, e);
+        f.hi[c][1] = pack_half2(b, d);
         if constexpr (QLO) {
             const float2 h0 = __half22float2(u32_as_h2(f.hi[c][0])), h1 = __half22float2(u32_as_h2(f.hi[c][1]));
-            f.lo[c][0] = pack_half2(a * u - h0.x, e * u - h0.y);
-            f.lo[c][1] = pack_half2(b * u - h1.x, d * u - h1.y);
+            f.lo[c][0] = pack_half2(a - h0.x, e - h0.y);
+            f.lo[c][1] = pack_half2(b - h1.x, d - h1.y);
         }
     }
     if constexpr (KT == KVQ_Q4_0) {
+        // the score of a key whose codes are all 8, block by block: what the offset adds
+        const uint32_t lo8[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
+        const uint32_t hi8[4] = {0x00800080u, 0x00800080u, 0x00800080u, 0x00800080u};
 #pragma unroll
         for (int b = 0; b < NS * 4; ++b) {
-            sum[b] += __shfl_xor_sync(0xffffffffu, sum[b], 1);
-            sum[b] += __shfl_xor_sync(0xffffffffu, sum[b], 2);
-            sum[b] *= -8.f / kUnit20;
-            f.corr[b][0] = __shfl_sync(0xffffffffu, sum[b], 8 * j);  // row 2j sits in lanes 8j .. 8j + 3
-            f.corr[b][1] = __shfl_sync(0xffffffffu, sum[b], 8 * j + 4);
+            float acc[4];
+            mma_16816_z(acc, lo8, f.hi[2 * b][0], f.hi[2 * b][1]);
+            mma_16816(acc, hi8, f.hi[2 * b + 1][0], f.hi[2 * b + 1][1]);
+            if constexpr (QLO) {
+                mma_16816(acc, lo8, f.lo[2 * b][0], f.lo[2 * b][1]);
+                mma_16816(acc, hi8, f.lo[2 * b + 1][0], f.lo[2 * b + 1][1]);
+            }
+            f.corr[b][0] = -acc[0];
+            f.corr[b][1] = -acc[1];
         }
     }
-    // never 0, so that a masked score stays -inf
+    // rows 2j, 2j + 1 sit in lanes 8j .. 8j + 7; never 0, so that a masked score stays -inf
     f.scale[0] = fmaxf(__shfl_sync(0xffffffffu, rs, 8 * j), 1e-36f);
     f.scale[1] = fmaxf(__shfl_sync(0xffffffffu, rs, 8 * j + 4), 1e-36f);
 }
@@ -253,6 +258,7 @@ __device__ __forceinline__ bool big_scales(const uint8_t *vs, int valid) {
     for (int sl = 0; sl < NS; ++sl) e |= *reinterpret_cast<const uint32_t *>(vs + sl * kScaleTile + lane * 4);
     e &= 0x40004000u;
     if (valid < kTileRows) {
+        keep_branch();
         const int k = 2 * (lane >> 3) + 8 * (lane & 1);
         e &= k >= valid ? 0u : (k + 1 >= valid ? 0x0000ffffu : 0xffffffffu);
     }
@@ -332,10 +338,9 @@ __device__ __forceinline__ void tile_o(const uint8_t *vc, const uint8_t *vs, con
 
 // ---- the walk over steps ----
 struct Walk {
-    int b;       // sequence
-    int unit;    // (KV head, row group) of it: h * groups + row group
-    int t;       // step of the unit
-    int tiles, steps, units, groups;  // of the sequence
+    int b, h, qg;  // sequence, KV head, row group: the unit
+    int t;         // step of the unit
+    int tiles, steps, groups;  // of the sequence
 };
 
 // sequence b, without tokens if it belongs to the chunk kernel
@@ -345,18 +350,18 @@ __device__ __forceinline__ PagedSeq split_seq(const PagedAttnParams &p, int b) {
     return s;
 }
 template <int TPS>
-__device__ __forceinline__ void walk_seq(Walk &w, const PagedAttnParams &p, int b) {
-    const PagedSeq s = split_seq(p, b);
+__device__ __forceinline__ void walk_seq(Walk &w, const int2 *shape, int b) {
+    const int2 s = shape[b];
     w.b = b;
-    w.tiles = (s.len + kTileRows - 1) / kTileRows;
-    w.steps = (w.tiles + TPS - 1) / TPS;
-    w.groups = (s.n * p.G + kRows - 1) / kRows;
-    w.units = w.groups * p.v.Hkv;
+    w.h = w.qg = w.t = 0;
+    w.tiles = s.x;
+    w.steps = (s.x + TPS - 1) / TPS;
+    w.groups = s.y;
 }
 // position at step x of all steps; pre[b] <= x < pre[n_seqs]
 template <int TPS>
-__device__ __noinline__ Walk walk_to(const PagedAttnParams &p, const int *pre, int x) {
-    int lo = 0, hi = p.v.n_seqs;  // last b with pre[b] <= x (it has steps, for pre[b + 1] > x)
+__device__ __forceinline__ Walk walk_to(const int *pre, const int2 *shape, int n_seqs, int x) {
+    int lo = 0, hi = n_seqs;  // last b with pre[b] <= x (it has steps, for pre[b + 1] > x)
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (pre[mid] <= x)
@@ -365,36 +370,40 @@ __device__ __noinline__ Walk walk_to(const PagedAttnParams &p, const int *pre, i
             hi = mid;
     }
     Walk w;
-    walk_seq<TPS>(w, p, lo);
-    const int r = x - pre[lo];
-    w.unit = r / w.steps;
-    w.t = r - w.unit * w.steps;
+    walk_seq<TPS>(w, shape, lo);
+    const unsigned r = x - pre[lo], unit = r / static_cast<unsigned>(w.steps);
+    w.t = r - unit * w.steps;
+    w.h = unit / static_cast<unsigned>(w.groups);
+    w.qg = unit - w.h * w.groups;
     return w;
 }
 // the first step of the next unit (a step follows: the caller counts)
 template <int TPS>
-__device__ __noinline__ Walk walk_next_unit(Walk w, const PagedAttnParams &p, const int *pre) {
+__device__ __forceinline__ void walk_next_unit(Walk &w, const int *pre, const int2 *shape, int Hkv) {
     w.t = 0;
-    if (++w.unit < w.units) return w;
+    if (++w.qg < w.groups) return;
+    w.qg = 0;
+    if (++w.h < Hkv) return;
     int b = w.b + 1;
     while (pre[b + 1] == pre[b]) ++b;
-    walk_seq<TPS>(w, p, b);
-    w.unit = 0;
-    return w;
+    walk_seq<TPS>(w, shape, b);
 }
 
-// Row r of a unit (row group qg of KV head h of sequence b): its output row, or -1.
+// Row r of a unit (row group qg of KV head h of sequence b): token i of the sequence, query head h G + g.
+// The quotient by G is exact in fp32: rr < 2^20 and the half keeps it off whole numbers.
 struct UnitRows {
-    size_t out0;  // first token * Hq + h * G
-    int Hq, G, r0, rows;
+    int first, Hq, h0, G, r0, rows;
+    float inv_g;
+    __device__ __forceinline__ int token(int r) const { return static_cast<int>((r0 + r + 0.5f) * inv_g); }
+    __device__ __forceinline__ int head(int r, int i) const { return h0 + r0 + r - i * G; }
     __device__ __forceinline__ long long out_row(int r) const {
-        const int rr = r0 + r;
-        return r < rows ? static_cast<long long>(out0) + static_cast<long long>(rr / G) * Hq + rr % G : -1;
+        if (r >= rows) return -1;
+        const int i = token(r);
+        return static_cast<long long>(first + i) * Hq + head(r, i);
     }
 };
 __device__ __forceinline__ UnitRows unit_rows(const PagedAttnParams &p, const PagedSeq &s, int h, int qg) {
-    return UnitRows{static_cast<size_t>(s.first) * p.Hq + static_cast<size_t>(h) * p.G, p.Hq, p.G, qg * kRows,
-                    min(kRows, s.n * p.G - qg * kRows)};
+    return UnitRows{s.first, p.Hq, h * p.G, p.G, qg * kRows, min(kRows, s.n * p.G - qg * kRows), 1.0f / p.G};
 }
 
 template <int KT, int VT, int NS, int DT>
@@ -412,6 +421,7 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
     // once per page and once per unit
     __shared__ Walk s_walk[C::WARPS][2];
     int *pre = reinterpret_cast<int *>(smem + C::OFF_PRE);
+    int2 *shape = reinterpret_cast<int2 *>(smem + C::OFF_SHAPE);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, j = lane & 3;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR) + warp * C::SLOTS;
     if (lane < C::SLOTS) mbar_init(full + lane, 1);
@@ -427,11 +437,13 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
         const int b0 = min(v.n_seqs, static_cast<int>(threadIdx.x) * per), b1 = min(v.n_seqs, b0 + per);
         int sum = 0;
         for (int b = b0; b < b1; ++b) {
-            Walk w;
-            walk_seq<TPS>(w, p, b);
+            PagedSeq q = paged_seq(v, b);
+            if (blockIdx.x == 0 && !q.ok) paged_error(v);
+            if (q.n >= p.split_below) q.n = 0;
+            const int tiles = (q.len + kTileRows - 1) / kTileRows, groups = (q.n * p.G + kRows - 1) / kRows;
+            shape[b] = make_int2(tiles, groups);
             pre[b] = sum;
-            sum += w.steps * w.units;
-            if (blockIdx.x == 0 && !paged_seq(v, b).ok) paged_error(v);
+            sum += (tiles + TPS - 1) / TPS * groups * v.Hkv;
         }
         int inc = sum;
 #pragma unroll
@@ -460,10 +472,7 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
     float o[NS * 8][4], corr[4], m_run[2], l[2], bias = kBias;
     if (lane == 0) s_unit[warp] = -1;
     // output rows of a unit
-    auto rows_of = [&](const Walk &w) {
-        const int h = w.unit / w.groups;
-        return unit_rows(p, split_seq(p, w.b), h, w.unit - h * w.groups);
-    };
+    auto rows_of = [&](const Walk &w) { return unit_rows(p, split_seq(p, w.b), w.h, w.qg); };
 
     // a finished segment in its registers: l summed over the keys' lanes, o in real units
     auto finish = [&]() {
@@ -522,7 +531,7 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
         uint8_t *const ring = smem + warp * (C::SLOTS * C::STEP);
         constexpr unsigned kAll = (1u << TPS) - 1u;
         {
-            const Walk w = walk_to<TPS>(p, pre, x0);
+            const Walk w = walk_to<TPS>(pre, shape, v.n_seqs, x0);
             if (lane == 0) *w_iss = *w_cur = w;
             __syncwarp();
         }
@@ -534,11 +543,10 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
         unsigned held = 0;  // bit slot * TPS + i: tile i of the slot's step was copied
         int tab = -1, tab_next = -1, tab0 = 0;
         auto load_tab = [&](const Walk &w, int e0) {
-            const int entries = (w.tiles + v.page_tiles - 1) / v.page_tiles;
-            return e0 + lane < entries ? __ldg(v.table + static_cast<size_t>(w.b) * v.stride + e0 + lane) : -1;
+            return (e0 + lane) * v.page_tiles < w.tiles ? __ldg(v.table + static_cast<size_t>(w.b) * v.stride + e0 + lane) : -1;
         };
         auto enter_unit = [&](const Walk &w) {
-            tab0 = w.t * TPS / v.page_tiles;
+            tab0 = static_cast<unsigned>(w.t * TPS) / static_cast<unsigned>(v.page_tiles);
             tab = load_tab(w, tab0);
             tab_next = load_tab(w, tab0 + 32);
         };
@@ -551,10 +559,10 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
             if (run == 0) {
                 Walk w = *w_iss;
                 if (w.t == w.steps) {
-                    w = walk_next_unit<TPS>(w, p, pre);
+                    walk_next_unit<TPS>(w, pre, shape, v.Hkv);
                     enter_unit(w);
                 }
-                const int h = w.unit / w.groups, t0 = w.t * TPS;
+                const int t0 = w.t * TPS;
                 auto entry = [&](int e) {  // e grows by at most one per call
                     if (e - tab0 >= 32) {
                         tab = tab_next;
@@ -564,9 +572,9 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
                     return __shfl_sync(0xffffffffu, tab, e - tab0);
                 };
                 auto record = [&](int page, int q) {
-                    return v.pool + ((static_cast<size_t>(page) * v.Hkv + h) * v.page_tiles + q) * T::BYTES;
+                    return v.pool + ((static_cast<size_t>(page) * v.Hkv + w.h) * v.page_tiles + q) * T::BYTES;
                 };
-                const int e = t0 / v.page_tiles, q = t0 - e * v.page_tiles;
+                const int e = static_cast<unsigned>(t0) / static_cast<unsigned>(v.page_tiles), q = t0 - e * v.page_tiles;
                 const int page = entry(e);
                 const bool in = page >= 0 && page < v.n_pages;
                 const int whole = min(v.page_tiles - q, w.tiles - t0) / TPS;  // steps of this page from here
@@ -627,18 +635,18 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
         while (true) {
             if (unit_left == 0) {  // a unit: its queries, empty accumulators
                 const Walk w = *w_cur;
-                const UnitRows rows = rows_of(w);
                 const PagedSeq s = split_seq(p, w.b);
+                const UnitRows rows = unit_rows(p, s, w.h, w.qg);
+                const int i0 = rows.token(g);
+                const X *qr = nullptr;
+                if (g < rows.rows)
+                    qr = static_cast<const X *>(p.q) + (s.first + i0) * p.q_stride + static_cast<size_t>(rows.head(g, i0)) * D;
                 len = s.len;
                 lim_min = s.len - s.n;  // the first token's position
-#pragma unroll
-                for (int i = 0; i < 2; ++i) lim[i] = lim_min + (rows.r0 + 2 * j + i) / p.G;
+                lim[0] = lim_min + rows.token(2 * j);
+                lim[1] = lim_min + rows.token(2 * j + 1);
                 key0 = w.t * TPS * kTileRows;
                 unit_left = w.steps - w.t;
-                const long long row = rows.out_row(g);  // token * Hq + head
-                const X *qr = nullptr;
-                if (row >= 0)
-                    qr = static_cast<const X *>(p.q) + (row / p.Hq) * p.q_stride + static_cast<size_t>(row % p.Hq) * D;
                 load_queries<KT, NS, C::QLO, DT>(f, qr, p.scale);
 #pragma unroll
                 for (int t = 0; t < NS * 8; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
@@ -669,6 +677,7 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < TPS; ++i) valid[i] = kTileRows;
             if (cut) {
+                keep_branch();
 #pragma unroll
                 for (int i = 0; i < TPS; ++i) {
                     valid[i] = ((got >> i) & 1u) ? len - key0 - i * kTileRows : 0;
@@ -740,6 +749,7 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
                 ph[1] = transpose8x8(ph[1]);
                 const uint8_t *tv = st + i * T::BYTES + T::OFF_V, *tvs = st + i * T::BYTES + T::OFF_VS;
                 if (cut) {
+                    keep_branch();
                     auto mask = [&](int k) { return k + 1 < valid[i] ? 0xffffffffu : (k < valid[i] ? 0x0000ffffu : 0u); };
                     tile_o<VT, NS, C::PLO, true>(tv, tvs, ph, pl, mask(2 * j), mask(2 * j + 8), o, corr);
                 } else {
@@ -762,7 +772,7 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
                     write_out(rows_of(w));
                 else
                     write_piece(gw * 2 + 1);
-                w = walk_next_unit<TPS>(w, p, pre);
+                walk_next_unit<TPS>(w, pre, shape, v.Hkv);
                 __syncwarp();
                 if (lane == 0) *w_cur = w;
                 __syncwarp();
@@ -771,18 +781,19 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
         }
         finish();
         if (lane == 0) {
-            s_unit[warp] = w_cur->unit;
+            s_unit[warp] = w_cur->h * w_cur->groups + w_cur->qg;
             s_b[warp] = w_cur->b;
         }
     }
     // ---- the warps of this CTA whose last segments are of one unit merge ----
     __syncthreads();
     const int unit = s_unit[warp], ub = unit >= 0 ? s_b[warp] : -1;
-    auto same = [&](int w) { return w >= 0 && w < C::WARPS && s_unit[w] == unit && s_b[w] == ub; };
     int first = warp, last = warp;
-    if (unit >= 0) {
-        while (same(first - 1)) --first;
-        while (same(last + 1)) ++last;
+    if (unit >= 0) {  // the run of warps around this one with the same unit
+        const bool eq = lane < C::WARPS && s_unit[lane] == unit && s_b[lane] == ub;
+        const unsigned other = ~__ballot_sync(0xffffffffu, eq);
+        first = 32 - __clz(other & ((1u << warp) - 1u));
+        last = __ffs(other & ~((2u << warp) - 1u)) - 2;
     }
     // the group holds steps [its first warp's segment start, the end of the unit or of its spans)
     const int steps = unit >= 0 ? w_cur->steps : 0, u0 = unit >= 0 ? pre[ub] + unit * steps : 0;
@@ -813,13 +824,15 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
     if (unit < 0 || first == last) return;
     // the group's warps share its rows and columns
     const int gt = (warp - first) * 32 + lane, gn = (last - first + 1) * 32;
-    for (int item = gt; item < kRows * (D / 4); item += gn) {
+    for (int item = gt; item < rows.rows * (D / 4); item += gn) {
         const int r = item / (D / 4), c = item % (D / 4);
         float M = -CUDART_INF_F;
+#pragma unroll 4
         for (int w = first; w <= last; ++w) M = fmaxf(M, s_ml[w][r]);
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
         float L = 0.f;
         if (M != -CUDART_INF_F) {
+#pragma unroll 4
             for (int w = first; w <= last; ++w) {
                 const float k = fast_ex2(s_ml[w][r] - M);
                 const float4 y = *reinterpret_cast<const float4 *>(buf + (w * kRows + r) * D + 4 * c);
@@ -953,6 +966,11 @@ cudaError_t launch_split_t(const PagedAttnParams &p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (!configured[dev]) {
         e = cudaFuncSetAttribute(paged_split_kernel<KT, VT, NS, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        // the merge runs right after the split kernel: with the same division of the SM's memory, no SM has
+        // to be drained and set up anew between the two
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(paged_merge_kernel<NS, DT>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     cudaSharedmemCarveoutMaxShared);
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
