@@ -564,7 +564,7 @@ class PagedCache:
                 result, qp, qs = q, 0, 0
             else:
                 hq = q.shape[1]
-                result = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+                result = torch.empty_like(q, memory_format=torch.contiguous_format) if q_out is None else q_out
                 qop, qos = self._rows(result, hq, "q_out", k.dtype)
                 _need(result.shape[0] == n, "q_out and q have the same tokens")
         _check(lib.kvq_paged_append(self.handle, ctypes.byref(batch), kp, vp, DTYPE_IDS[k.dtype], ks, vs, ra, qp, hq, qs, qop,
@@ -604,7 +604,7 @@ class PagedCache:
         else:
             _need(workspace.device == self.device and workspace.is_contiguous(), "workspace: contiguous, on the cache's device")
         if out is None:
-            out = torch.empty((n, hq, d), dtype=q.dtype, device=self.device)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         else:
             _need(out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous() and out.device == self.device,
                   "out: contiguous, like q")

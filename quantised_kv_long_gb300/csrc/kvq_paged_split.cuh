@@ -11,7 +11,8 @@
 // shared-memory slots, filled by one bulk copy per tile record (or per pair in one page), so no
 // warp waits for another until the end, where the warps that worked on one unit merge in shared
 // memory.  What is not the whole of its unit goes to the workspace as a piece (m, l, o), and a
-// second kernel merges the pieces; a unit that lay in one CTA is written at once.
+// second kernel merges the pieces; a unit that lay in one CTA is written at once.  Short contexts in few
+// units take one CTA per unit instead (UNITS): no sums over the batch, no pieces and no second kernel.
 //
 // Products.  Keys and values are the A operands of mma.sync m16n8k16 (16 keys, or 16 values, by
 // 16) and the query rows its eight columns, so one instruction serves 16 keys x 8 rows without
@@ -408,7 +409,7 @@ __device__ __forceinline__ UnitRows unit_rows(const PagedAttnParams &p, const Pa
 
 template <int KT, int VT, int NS, int DT>
 __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
-    paged_split_kernel(const PagedAttnParams p, const SplitWork work) {
+    paged_split_kernel(const PagedAttnParams p, const SplitWork work, const int unit_groups) {
     using C = SplitCfg<KT, VT, NS, DT>;
     using T = typename C::T;
     using X = typename Act<DT>::type;
@@ -430,45 +431,74 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
-    // ---- steps before each sequence: every CTA adds them up for itself ----
     const PagedView &v = p.v;
-    {
-        const int per = (v.n_seqs + C::THREADS - 1) / C::THREADS;
-        const int b0 = min(v.n_seqs, static_cast<int>(threadIdx.x) * per), b1 = min(v.n_seqs, b0 + per);
-        int sum = 0;
-        for (int b = b0; b < b1; ++b) {
-            PagedSeq q = paged_seq(v, b);
-            if (blockIdx.x == 0 && !q.ok) paged_error(v);
-            if (q.n >= p.split_below) q.n = 0;
-            const int tiles = (q.len + kTileRows - 1) / kTileRows, groups = (q.n * p.G + kRows - 1) / kRows;
-            shape[b] = make_int2(tiles, groups);
-            pre[b] = sum;
-            sum += (tiles + TPS - 1) / TPS * groups * v.Hkv;
+    int x0, x1, span = 0, total = 0;  // this warp's steps
+    Walk w0;                          // where they start
+    if (unit_groups > 0) {
+        // ---- one unit per CTA, its steps shared by the warps ----
+        const int r = blockIdx.x / unit_groups;
+        w0.qg = blockIdx.x - r * unit_groups;
+        w0.b = r / v.Hkv;
+        w0.h = r - w0.b * v.Hkv;
+        const PagedSeq q = split_seq(p, w0.b);
+        if (threadIdx.x == 0 && w0.h == 0 && w0.qg == 0 && !paged_seq(v, w0.b).ok) paged_error(v);
+        w0.tiles = (q.len + kTileRows - 1) / kTileRows;
+        w0.steps = (w0.tiles + TPS - 1) / TPS;
+        w0.groups = (q.n * p.G + kRows - 1) / kRows;
+        if (w0.qg >= w0.groups) return;
+        if (w0.steps == 0) {  // nothing to attend to
+            const UnitRows rows = unit_rows(p, q, w0.h, w0.qg);
+            for (int i = threadIdx.x; i < rows.rows * (D / 4); i += C::THREADS) {
+                const long long row = rows.out_row(i / (D / 4));
+                Act<DT>::store4(static_cast<X *>(p.out) + row * D + i % (D / 4) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+                if (i % (D / 4) == 0 && p.lse) p.lse[row] = -CUDART_INF_F;
+            }
+            return;
         }
-        int inc = sum;
+        const int share = (w0.steps + C::WARPS - 1) / C::WARPS;
+        x0 = min(w0.steps, warp * share);
+        x1 = min(w0.steps, x0 + share);
+        w0.t = x0;
+    } else {
+        // ---- steps before each sequence: every CTA adds them up for itself ----
+        {
+            const int per = (v.n_seqs + C::THREADS - 1) / C::THREADS;
+            const int b0 = min(v.n_seqs, static_cast<int>(threadIdx.x) * per), b1 = min(v.n_seqs, b0 + per);
+            int sum = 0;
+            for (int b = b0; b < b1; ++b) {
+                PagedSeq q = paged_seq(v, b);
+                if (blockIdx.x == 0 && !q.ok) paged_error(v);
+                if (q.n >= p.split_below) q.n = 0;
+                const int tiles = (q.len + kTileRows - 1) / kTileRows, groups = (q.n * p.G + kRows - 1) / kRows;
+                shape[b] = make_int2(tiles, groups);
+                pre[b] = sum;
+                sum += (tiles + TPS - 1) / TPS * groups * v.Hkv;
+            }
+            int inc = sum;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            if (lane == 31) s_scan[warp] = inc;
+            __syncthreads();
+            int before = inc - sum;
+            for (int w = 0; w < warp; ++w) before += s_scan[w];
+            for (int b = b0; b < b1; ++b) pre[b] += before;
+            if (threadIdx.x == C::THREADS - 1) pre[v.n_seqs] = before + sum;
+            __syncthreads();
         }
-        if (lane == 31) s_scan[warp] = inc;
-        __syncthreads();
-        int before = inc - sum;
-        for (int w = 0; w < warp; ++w) before += s_scan[w];
-        for (int b = b0; b < b1; ++b) pre[b] += before;
-        if (threadIdx.x == C::THREADS - 1) pre[v.n_seqs] = before + sum;
-        __syncthreads();
+        total = pre[v.n_seqs];
+        span = (total + static_cast<int>(gridDim.x) * C::WARPS - 1) / (static_cast<int>(gridDim.x) * C::WARPS);
+        if (blockIdx.x == 0) {  // for the merge
+            for (int b = threadIdx.x; b <= v.n_seqs; b += C::THREADS) work.pre[b] = pre[b];
+            if (threadIdx.x == 0) work.pre[v.n_seqs + 1] = span;
+        }
+        const long long x0l = static_cast<long long>(blockIdx.x * C::WARPS + warp) * span;
+        x0 = x0l < total ? static_cast<int>(x0l) : total;
+        x1 = min(total, x0 + span);
+        if (x0 < x1) w0 = walk_to<TPS>(pre, shape, v.n_seqs, x0);
     }
-    const int total = pre[v.n_seqs];
-    const int span = (total + static_cast<int>(gridDim.x) * C::WARPS - 1) / (static_cast<int>(gridDim.x) * C::WARPS);
-    if (blockIdx.x == 0) {  // for the merge
-        for (int b = threadIdx.x; b <= v.n_seqs; b += C::THREADS) work.pre[b] = pre[b];
-        if (threadIdx.x == 0) work.pre[v.n_seqs + 1] = span;
-    }
-    const int gw = blockIdx.x * C::WARPS + warp;
-    const long long x0l = static_cast<long long>(gw) * span;
-    const int x0 = x0l < total ? static_cast<int>(x0l) : total, x1 = min(total, x0 + span);
-
     float o[NS * 8][4], corr[4], m_run[2], l[2], bias = kBias;
     if (lane == 0) s_unit[warp] = -1;
     // output rows of a unit
@@ -530,11 +560,8 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
     if (x0 < x1) {
         uint8_t *const ring = smem + warp * (C::SLOTS * C::STEP);
         constexpr unsigned kAll = (1u << TPS) - 1u;
-        {
-            const Walk w = walk_to<TPS>(pre, shape, v.n_seqs, x0);
-            if (lane == 0) *w_iss = *w_cur = w;
-            __syncwarp();
-        }
+        if (lane == 0) *w_iss = *w_cur = w0;
+        __syncwarp();
         // ---- the issuing side runs SLOTS steps ahead.  Steps whose tiles follow one another in a page form a
         // run, found once: within it a step is one copy from `src`.  A lane holds one entry of the unit's
         // block table (entries tab0 .. tab0 + 31), the next 32 are on their way. ----
@@ -771,7 +798,7 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
                 if (!first || w.t == 0)
                     write_out(rows_of(w));
                 else
-                    write_piece(gw * 2 + 1);
+                    write_piece((blockIdx.x * C::WARPS + warp) * 2 + 1);
                 walk_next_unit<TPS>(w, pre, shape, v.Hkv);
                 __syncwarp();
                 if (lane == 0) *w_cur = w;
@@ -796,11 +823,11 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
         last = __ffs(other & ~((2u << warp) - 1u)) - 2;
     }
     // the group holds steps [its first warp's segment start, the end of the unit or of its spans)
-    const int steps = unit >= 0 ? w_cur->steps : 0, u0 = unit >= 0 ? pre[ub] + unit * steps : 0;
+    const int steps = unit >= 0 ? w_cur->steps : 0, u0 = unit >= 0 && unit_groups == 0 ? pre[ub] + unit * steps : 0;
     UnitRows rows{};
     if (unit >= 0) rows = rows_of(*w_cur);
     const int g0 = max(u0, (blockIdx.x * C::WARPS + first) * span), g1 = min(total, (static_cast<int>(blockIdx.x) * C::WARPS + last + 1) * span);
-    const bool whole = unit >= 0 && g0 == u0 && g1 >= u0 + steps;
+    const bool whole = unit >= 0 && (unit_groups > 0 || (g0 == u0 && g1 >= u0 + steps));
     if (unit >= 0 && first == last) {
         if (whole)
             write_out(rows);
@@ -955,6 +982,17 @@ __global__ void __launch_bounds__(NS * 32 * kMergeWays)
 }
 
 constexpr int kSplitMaxWarps = 16;
+// One CTA per unit, or equal spans?  A unit costs its CTA about 4.5 us + 4.9 us per 1024 keys; equal spans
+// cost 9.5 us (sums over the batch, the merge) and then 2 us + 4.7 us per 1024 keys for each unit per SM
+// (q4_0, 128-wide; measured over 1 to 128 sequences of 8 KV heads, 128 to 4096 positions: 8 units of 128 /
+// 512 / 1024 keys 5.5 / 7.4 / 10.3 against 9.9 / 10.7 / 11.0 us, 128 units of 2048 keys 15.9 against 20.0,
+// 304 units of 1024 keys 20.8 against 23.7, 512 units of 512 keys 28.4 against 25.0).  Lengths are known
+// here by their bound alone, and a CTA per unit waits for the longest, so the bound stays near the point
+// where the two are equal for even lengths in one wave, and below it in two.
+inline bool unit_per_cta(long long units, int max_len, int sms) {
+    if (units <= sms) return max_len <= 1024 + 1024 * units / sms;
+    return units <= 2ll * sms && 2 * units >= 3ll * sms && max_len <= 1024;
+}
 
 template <int KT, int VT, int NS, int DT>
 cudaError_t launch_split_t(const PagedAttnParams &p, cudaStream_t stream) {
@@ -984,11 +1022,17 @@ cudaError_t launch_split_t(const PagedAttnParams &p, cudaStream_t stream) {
     if (most < 1) return cudaErrorInvalidValue;
     for (int b = 0; b < p.v.n_seqs; b += most) {
         const PagedAttnParams q = paged_some(p, b, most);
-        e = launch_dependent(paged_split_kernel<KT, VT, NS, DT>, dim3(sms), C::THREADS, C::SMEM, stream, q, work);
+        const long long units = static_cast<long long>(q.v.n_seqs) * p.v.Hkv * max_groups;
+        if (unit_per_cta(units, p.v.max_len, sms)) {
+            e = launch_dependent(paged_split_kernel<KT, VT, NS, DT>, dim3(static_cast<unsigned>(units)), C::THREADS, C::SMEM, stream,
+                                 q, work, max_groups);
+            if (e != cudaSuccess) return e;
+            continue;
+        }
+        e = launch_dependent(paged_split_kernel<KT, VT, NS, DT>, dim3(sms), C::THREADS, C::SMEM, stream, q, work, 0);
         if (e != cudaSuccess) return e;
-        const long long units = static_cast<long long>(q.v.n_seqs) * p.v.Hkv * max_groups * kRows;
-        e = launch_dependent(paged_merge_kernel<NS, DT>, dim3(static_cast<unsigned>(units)), NS * 32 * kMergeWays, 0, stream, q,
-                             work, static_cast<int>(C::WARPS), static_cast<int>(C::TPS), max_groups);
+        e = launch_dependent(paged_merge_kernel<NS, DT>, dim3(static_cast<unsigned>(units * kRows)), NS * 32 * kMergeWays, 0, stream,
+                             q, work, static_cast<int>(C::WARPS), static_cast<int>(C::TPS), max_groups);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
