@@ -426,6 +426,10 @@ def combine(part_o, part_m, part_l, out=None, lse=None, stream=None):
 
 
 # ---- paged cache ----
+def _current_device():
+    return torch._C._cuda_getDevice()
+
+
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
@@ -470,6 +474,7 @@ class PagedCache:
         self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
+        self._index = self.device.index
         self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = n_pages, page_size, n_kv_heads, head_dim
         self.type_k, self.type_v = type_k, type_v
         pool_bytes, state_bytes = paged_size(n_pages, page_size, n_kv_heads, head_dim, type_k, type_v)
@@ -525,19 +530,19 @@ class PagedCache:
         if stream is not None:
             with torch.cuda.stream(stream):
                 return fn(*args)
-        if torch.cuda.current_device() != self.device.index:
-            with torch.cuda.device(self.device):
-                return fn(*args)
-        return fn(*args)
+        with torch.cuda.device(self.device):
+            return fn(*args)
 
     def _stream(self):
         # the handle alone: torch.cuda.current_stream() also makes a Stream object, 3 us a call
-        return torch._C._cuda_getCurrentRawStream(self.device.index)
+        return torch._C._cuda_getCurrentRawStream(self._index)
 
     def append(self, k, v, block_table, lens, cu_q=None, max_q=None, max_len=None, rope=None, positions=None, q=None,
                q_out=None, stream=None):
         """Rotate (rope) and quantise k, v [n_tokens, Hkv, D] into their pages.  With q
         [n_tokens, Hq, D] also returns the rotated queries (q_out, which may be q)."""
+        if stream is None and _current_device() == self._index:
+            return self._append(k, v, block_table, lens, cu_q, max_q, max_len, rope, positions, q, q_out)
         return self._call(stream, self._append, k, v, block_table, lens, cu_q, max_q, max_len, rope, positions, q, q_out)
 
     def _append(self, k, v, block_table, lens, cu_q, max_q, max_len, rope, positions, q, q_out):
@@ -574,6 +579,8 @@ class PagedCache:
     def gather(self, block_table, lens, n_tokens, cu_q=None, max_q=None, max_len=None, dtype=torch.float16, stream=None):
         """The values of the batch's rows: (k, v), each [n_tokens, Hkv, D] of `dtype`.  Rows of
         padding tokens are not written."""
+        if stream is None and _current_device() == self._index:
+            return self._gather(block_table, lens, n_tokens, cu_q, max_q, max_len, dtype)
         return self._call(stream, self._gather, block_table, lens, n_tokens, cu_q, max_q, max_len, dtype)
 
     def _gather(self, block_table, lens, n_tokens, cu_q, max_q, max_len, dtype):
@@ -592,6 +599,8 @@ class PagedCache:
         (contiguous), and with return_lse also lse fp32 [n_tokens, Hq].  Rows of padding tokens
         are not written.  `workspace`: a uint8 CUDA tensor of workspace_bytes(...) bytes used by
         no other call at the same time (default: one made for this call)."""
+        if stream is None and _current_device() == self._index:
+            return self._attention(q, block_table, lens, cu_q, max_q, max_len, scale, out, return_lse, workspace)
         return self._call(stream, self._attention, q, block_table, lens, cu_q, max_q, max_len, scale, out, return_lse, workspace)
 
     def _attention(self, q, block_table, lens, cu_q, max_q, max_len, scale, out, return_lse, workspace):

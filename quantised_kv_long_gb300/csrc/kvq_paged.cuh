@@ -219,7 +219,7 @@ struct PagedAttnParams {
     float scale;
     void *workspace;
     // sequences with fewer tokens than this belong to the split kernel, the others to the chunk kernel
-    int split_below;
+    int from_q;
 };
 
 cudaError_t launch_paged_append(int type_k, int type_v, int D, int dtype, const PagedAppendParams &p, cudaStream_t s);
@@ -235,7 +235,7 @@ cudaError_t paged_split_workspace(int D, size_t *bytes);
 // many queries per sequence (kvq_paged_chunk.cuh)
 cudaError_t launch_paged_chunk_f16(int type_k, int type_v, int D, const PagedAttnParams &p, cudaStream_t s);
 cudaError_t launch_paged_chunk_bf16(int type_k, int type_v, int D, const PagedAttnParams &p, cudaStream_t s);
-cudaError_t paged_chunk_workspace(int D, size_t *bytes);
+cudaError_t paged_chunk_workspace(int D, const PagedAttnParams &p, size_t *bytes);
 
 // ---- what the attention launches share ----
 constexpr int kPagedMaxDevices = 64;

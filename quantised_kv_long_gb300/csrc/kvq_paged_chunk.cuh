@@ -17,6 +17,11 @@
 // than kChunkDrift.  S of the next block is computed while the softmax of this one runs (S and P have
 // their own columns).
 //
+// Lifted.  Converting costs about as many instructions as the softmax of 256 rows, once per unit; so a kernel
+// before this one makes the operands of every block once, in the order the MMA reads them, and the chunk
+// kernel streams them from the workspace (LIFT) without converters: 32 KB per step and head of 128 instead
+// of 9 to 32 KB of codes.  Where that workspace would be too large (kLiftBytes) the converters run inside.
+//
 // Orders.  The values of K^ and Q sit in the order 0, 2, 1, 3 within each four (as the bytes of a code
 // word come out), and the rows of V^ (columns of O) in the order 0, 2, .., 14, 1, 3, .., 15 within each
 // sixteen, so that a warp's stores of V^ fill whole core matrices; the epilogue puts them back.
@@ -147,45 +152,242 @@ __device__ __forceinline__ int core_at(int row, int k, int kext) {
     return (row >> 3) * (kext * 16) + (k >> 3) * 128 + (row & 7) * 16 + (k & 7) * 2;
 }
 
-template <int KT, int VT, int NS>
+// ---- codes to operands ----
+constexpr int kChunkKeys = 64, kChunkTiles = kChunkKeys / kTileRows;
+
+// Rows of a block's tiles in use: bit i of `got` set if tile i has a page; the sequence ends `left` rows
+// after the block's first.
+struct BlockRows {
+    int got, left;
+    __device__ __forceinline__ int of(int i) const {
+        return ((got >> i) & 1) ? max(0, min(kTileRows, left - i * kTileRows)) : 0;
+    }
+};
+// a pair of halves of rows r, r + 1, those from `use` on replaced by 0
+__device__ __forceinline__ uint32_t cut_pair(uint32_t x, int r, int use) {
+    return r >= use ? 0u : (r + 1 >= use ? (x & 0xffffu) : x);
+}
+__device__ __forceinline__ float pow2i_f(int e) { return __int_as_float((127 + e) << 23); }
+__device__ __forceinline__ __half2 half_twice(uint32_t pair, int upper) {  // one half of a pair, twice
+    return u32_as_h2(perm(pair, 0u, upper ? 0x3232u : 0x1010u));
+}
+// q8_0 codes (sign in bit 15, magnitude in the low bits: a subnormal q 2^-24) times 2^14: q 2^-10, exactly
+__device__ __forceinline__ __half2 q8_small(uint32_t x) { return __hmul2(u32_as_h2(x & 0x807f807fu), __float2half2_rn(16384.0f)); }
+// q4_0 codes in the low or high nibble of each half's low byte: c - 8
+__device__ __forceinline__ __half2 q4_low(uint32_t x) {
+    return __hsub2(u32_as_h2((x & 0x000f000fu) | 0x64006400u), __float2half2_rn(1032.0f));
+}
+__device__ __forceinline__ __half2 q4_high(uint32_t x) {
+    return __hfma2(u32_as_h2((x & 0x00f000f0u) | 0x64006400u), __float2half2_rn(0.0625f), __float2half2_rn(-72.0f));
+}
+
+// Exponent e >= 0 with |value| 2^-e below 2^14 (q4_0) or 2^12 (q8_0, whose scale meets codes times 2^-10) over
+// the block's rows in use; at most 11.  OFF: the scales in a tile record.  By a whole warp.
+template <int TYPE, int OFF, int NS, class TileAt>
+__device__ __forceinline__ int block_exp(TileAt tile, const BlockRows &use) {
+    if constexpr (TYPE == KVQ_F16) {
+        return 0;
+    } else {
+        const float cmax = TYPE == KVQ_Q8_0 ? 127.f : 8.f;
+        constexpr int most = TYPE == KVQ_Q8_0 ? 12 : 14;
+        const int lane = threadIdx.x & 31;
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+            const int gi = k * 32 + lane, i = gi / (8 * NS), in = gi % (8 * NS);  // tile, 16-byte group of its scales
+            uint4 w = *reinterpret_cast<const uint4 *>(tile(i) + OFF + in * 16);
+            const int n = use.of(i), ka = 2 * ((in & 7) >> 1);
+            if (n < kTileRows) {
+                keep_branch();
+                w = make_uint4(cut_pair(w.x, ka, n), cut_pair(w.y, ka + 8, n), cut_pair(w.z, ka, n), cut_pair(w.w, ka + 8, n));
+            }
+            const __half2 a = __hmax2(__habs2(u32_as_h2(w.x)), __habs2(u32_as_h2(w.y)));
+            const __half2 b = __hmax2(__habs2(u32_as_h2(w.z)), __habs2(u32_as_h2(w.w)));
+            m = h2_as_u32(__hmax2(u32_as_h2(m), __hmax2(a, b)));
+        }
+        const float2 f = __half22float2(u32_as_h2(m));
+        float top = fmaxf(f.x, f.y) * cmax;
+        if (!__any_sync(0xffffffffu, top > static_cast<float>(1 << most))) return 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        return min(11, max(0, ilogbf(top) - (most - 1)));
+    }
+}
+
+// K^ of a block times 2^-e, by warps cw, cw + nw, ..: rows past the sequence's end may become anything (their
+// scores are masked).  tile(i): record of tile i; kh: the operand, shared or global memory.
+template <int KT, int VT, int NS, class TileAt>
+__device__ __forceinline__ void convert_keys(TileAt tile, uint8_t *kh, int e, int cw, const int nw) {
+    using T = PagedTile<KT, VT, NS>;
+    constexpr int D = T::D;
+    const int lane = threadIdx.x & 31, n = lane >> 2, jd = lane & 3;  // key n (and n + 8) of the tile, 4-value group jd
+    const __half2 fk = __float2half2_rn(pow2i_f(KT == KVQ_Q8_0 ? 10 - e : -e));
+    uint8_t *lane_at = kh + (jd >> 1) * 128 + n * 16 + (jd & 1) * 8;  // core_at(n, 4 jd, D)
+    auto put = [&](int at, __half2 c02, __half2 c13, __half2 d2) {
+        *reinterpret_cast<uint2 *>(lane_at + at) = make_uint2(h2_as_u32(__hmul2(c02, d2)), h2_as_u32(__hmul2(c13, d2)));
+    };
+    // core_at(16 i + n + 8 s8, dim + 4 jd, D) less lane_at, for dim a multiple of 16
+    auto at = [](int i, int s8, int dim) { return (2 * i + s8) * (D * 16) + dim * 16; };
+    if constexpr (KT == KVQ_Q8_0) {
+#pragma unroll 4
+        for (int wu = cw; wu < kChunkTiles * NS * 4; wu += nw) {
+            const int ts = wu >> 2, b = wu & 3, i = ts / NS, sl = ts % NS, dim = sl * kSlice + 32 * b;
+            const uint8_t *t = tile(i);
+            const uint4 c = *reinterpret_cast<const uint4 *>(t + sl * 2048 + (b * 32 + lane) * 16);
+            const uint2 sc = *reinterpret_cast<const uint2 *>(t + T::OFF_KS + sl * kScaleTile + (n >> 1) * 32 + b * 8);
+            const __half2 da = __hmul2(half_twice(sc.x, n & 1), fk), db = __hmul2(half_twice(sc.y, n & 1), fk);
+            auto lo = [](uint32_t w) { return q8_small(perm(w, 0u, 0xA280u)); };
+            auto hi = [](uint32_t w) { return q8_small(perm(w, 0u, 0xB391u)); };
+            put(at(i, 0, dim), lo(c.x), hi(c.x), da);
+            put(at(i, 0, dim + 16), lo(c.y), hi(c.y), da);
+            put(at(i, 1, dim), lo(c.z), hi(c.z), db);
+            put(at(i, 1, dim + 16), lo(c.w), hi(c.w), db);
+        }
+    } else if constexpr (KT == KVQ_Q4_0) {
+#pragma unroll 2
+        for (int wu = cw; wu < kChunkTiles * NS * 2; wu += nw) {
+            const int ts = wu >> 1, b2 = wu & 1, i = ts / NS, sl = ts % NS;
+            const uint8_t *t = tile(i);
+            const uint4 c = *reinterpret_cast<const uint4 *>(t + sl * 1024 + (b2 * 32 + lane) * 16);
+            const uint4 sc = *reinterpret_cast<const uint4 *>(t + T::OFF_KS + sl * kScaleTile + (n >> 1) * 32 + b2 * 16);
+            const uint32_t cs[4] = {c.x, c.y, c.z, c.w}, ss[4] = {sc.x, sc.y, sc.z, sc.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {  // block 2 b2 + q / 2, key n + 8 (q % 2)
+                const int dim = sl * kSlice + 64 * b2 + 32 * (q >> 1);
+                const __half2 d2 = __hmul2(half_twice(ss[q], n & 1), fk);
+                const uint32_t odd = cs[q] >> 8;
+                put(at(i, q & 1, dim), q4_low(cs[q]), q4_low(odd), d2);
+                put(at(i, q & 1, dim + 16), q4_high(cs[q]), q4_high(odd), d2);
+            }
+        }
+    } else {
+#pragma unroll 4
+        for (int wu = cw; wu < kChunkTiles * NS * 8; wu += nw) {
+            const int ts = wu >> 3, ch = wu & 7, i = ts / NS, sl = ts % NS, dim = sl * kSlice + 32 * (ch >> 1);
+            const uint4 c = *reinterpret_cast<const uint4 *>(tile(i) + sl * 4096 + (ch * 32 + lane) * 16);
+            *reinterpret_cast<uint2 *>(lane_at + at(i, ch & 1, dim)) = make_uint2(c.x, c.y);
+            *reinterpret_cast<uint2 *>(lane_at + at(i, ch & 1, dim + 16)) = make_uint2(c.z, c.w);
+        }
+    }
+}
+
+// V^ of a block times 2^-e: rows past the sequence's end may hold any bits and become 0.
+template <int KT, int VT, int NS, class TileAt>
+__device__ __forceinline__ void convert_values(TileAt tile, uint8_t *vh, int e, const BlockRows &use, int cw, const int nw) {
+    using T = PagedTile<KT, VT, NS>;
+    const int lane = threadIdx.x & 31, np = lane >> 2, j = lane & 3;
+    const __half2 fv = __float2half2_rn(pow2i_f(VT == KVQ_Q8_0 ? 10 - e : -e));
+    uint8_t *lane_at = vh + np * 16 + j * 4;  // row np of a core matrix, keys 2j, 2j + 1
+    // value dim + 2 np + odd of keys 16 i + 2j, + 1 (and + 8, + 9): row (dim / 8 + odd) * 8 + np
+    auto at = [](int i, int dim, int odd) { return ((dim >> 3) + odd) * (kChunkKeys * 16) + 2 * i * 128; };
+    auto put = [&](int a, __half2 ca, __half2 cb, __half2 da, __half2 db) {
+        *reinterpret_cast<uint32_t *>(lane_at + a) = h2_as_u32(__hmul2(ca, da));
+        *reinterpret_cast<uint32_t *>(lane_at + a + 128) = h2_as_u32(__hmul2(cb, db));
+    };
+    if constexpr (VT == KVQ_Q8_0) {
+#pragma unroll 4
+        for (int wu = cw; wu < kChunkTiles * NS * 4; wu += nw) {
+            const int ts = wu >> 2, b = wu & 3, i = ts / NS, sl = ts % NS, n = use.of(i);
+            const uint8_t *t = tile(i);
+            const uint4 c = *reinterpret_cast<const uint4 *>(t + T::OFF_V + sl * 2048 + (b * 32 + lane) * 16);
+            const uint2 sc = *reinterpret_cast<const uint2 *>(t + T::OFF_VS + sl * kScaleTile + j * 32 + b * 8);
+            const __half2 da = __hmul2(u32_as_h2(cut_pair(sc.x, 2 * j, n)), fv), db = __hmul2(u32_as_h2(cut_pair(sc.y, 2 * j + 8, n)), fv);
+            const uint32_t cs[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                put(at(i, sl * kSlice + 32 * b + 16 * (q >> 1), q & 1), q8_small(perm(cs[q], 0u, 0xA280u)), q8_small(perm(cs[q], 0u, 0xB391u)), da, db);
+        }
+    } else if constexpr (VT == KVQ_Q4_0) {
+#pragma unroll 2
+        for (int wu = cw; wu < kChunkTiles * NS * 2; wu += nw) {
+            const int ts = wu >> 1, b2 = wu & 1, i = ts / NS, sl = ts % NS, n = use.of(i);
+            const uint8_t *t = tile(i);
+            const uint4 c = *reinterpret_cast<const uint4 *>(t + T::OFF_V + sl * 1024 + (b2 * 32 + lane) * 16);
+            const uint4 sc = *reinterpret_cast<const uint4 *>(t + T::OFF_VS + sl * kScaleTile + j * 32 + b2 * 16);
+            const __half2 d[4] = {__hmul2(u32_as_h2(cut_pair(sc.x, 2 * j, n)), fv), __hmul2(u32_as_h2(cut_pair(sc.y, 2 * j + 8, n)), fv),
+                                  __hmul2(u32_as_h2(cut_pair(sc.z, 2 * j, n)), fv), __hmul2(u32_as_h2(cut_pair(sc.w, 2 * j + 8, n)), fv)};
+            const uint32_t cs[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {  // block 2 b2 + q / 2, value 2 np + q % 2 (and + 16)
+                const int dim = sl * kSlice + 64 * b2 + 32 * (q >> 1);
+                const uint32_t odd = cs[q] >> 8;
+                put(at(i, dim, q & 1), q4_low(cs[q]), q4_low(odd), d[2 * (q >> 1)], d[2 * (q >> 1) + 1]);
+                put(at(i, dim + 16, q & 1), q4_high(cs[q]), q4_high(odd), d[2 * (q >> 1)], d[2 * (q >> 1) + 1]);
+            }
+        }
+    } else {
+#pragma unroll 4
+        for (int wu = cw; wu < kChunkTiles * NS * 8; wu += nw) {
+            const int ts = wu >> 3, ch = wu & 7, i = ts / NS, sl = ts % NS, n = use.of(i);
+            const uint4 c = *reinterpret_cast<const uint4 *>(tile(i) + T::OFF_V + sl * 4096 + (ch * 32 + lane) * 16);
+            const int dim = sl * kSlice + 32 * (ch >> 1) + 16 * (ch & 1);
+#pragma unroll
+            for (int odd = 0; odd < 2; ++odd) {
+                uint8_t *to = lane_at + at(i, dim, odd);
+                *reinterpret_cast<uint32_t *>(to) = cut_pair(odd ? c.z : c.x, 2 * j, n);
+                *reinterpret_cast<uint32_t *>(to + 128) = cut_pair(odd ? c.w : c.y, 2 * j + 8, n);
+            }
+        }
+    }
+}
+
+template <int KT, int VT, int NS, bool LIFT>
 struct ChunkCfg {
     using T = PagedTile<KT, VT, NS>;
-    static constexpr int D = T::D, M = 128, NK = 64, TILES = NK / kTileRows;
+    static constexpr int D = T::D, M = 128, NK = kChunkKeys, TILES = kChunkTiles;
     static constexpr int NT = NS == 1 ? 2 : 1;  // tiles of 128 rows per unit
     static constexpr int ROWS = NT * M;
-    static constexpr int STAGE = TILES * T::BYTES;
-    static constexpr int KHAT = NK * D * 2, VHAT = NK * D * 2;
+    static constexpr int KHAT = NK * D * 2, VHAT = NK * D * 2, IMAGE = KHAT + VHAT;
     static constexpr int QSM = NT == 2 ? M * D * 2 : 0;  // Q of tile 1 (tile 0's is in tensor memory)
-    static constexpr int LIMIT = 232448 - 2048;          // of the CTA's shared memory, barriers and statics kept back
-    static constexpr int KB = 2;
-    // two V^ buffers where two raw stages still fit, else one
-    static constexpr int VB = (LIMIT - QSM - KB * KHAT - 2 * VHAT) / STAGE >= 2 ? 2 : 1;
+    static constexpr int LIMIT = 232448 - 3072;          // of the CTA's shared memory, barriers and statics kept back
+    // operand buffers: all that fit when lifted, else two of each, or one of V^ where two raw stages would not fit
+    static constexpr int STAGE = LIFT ? 1 : TILES * T::BYTES;
+    static constexpr int KB = LIFT ? (LIMIT - QSM) / IMAGE : 2;
+    static constexpr int VB = LIFT ? KB : ((LIMIT - QSM - KB * KHAT - 2 * VHAT) / STAGE >= 2 ? 2 : 1);
     static constexpr int OPS = QSM + KB * KHAT + VB * VHAT;
     static constexpr int STAGES_RAW = (LIMIT - OPS) / STAGE;
-    static constexpr int STAGES = STAGES_RAW > 4 ? 4 : STAGES_RAW;
+    static constexpr int STAGES = LIFT ? 0 : (STAGES_RAW > 4 ? 4 : STAGES_RAW);  // of raw tiles
     static constexpr int OFF_Q = STAGES * STAGE, OFF_K = OFF_Q + QSM, OFF_V = OFF_K + KB * KHAT;
     static constexpr int SMEM = OFF_V + VB * VHAT;
     // tensor memory columns: O of each tile, S of each, P of each, Q of tile 0
     static constexpr int T_O = 0, T_S = NT * D, T_P = T_S + NT * NK, T_Q = T_P + NT * NK / 2;
     static_assert(T_Q + D / 2 <= 512, "tensor memory");
-    static_assert(STAGES >= 2 && SMEM <= LIMIT, "shared memory");
-    static constexpr int SOFT0 = 4, CONV0 = SOFT0 + 4 * NT, CONV_WARPS = 8;  // first softmax / converter warp
-    static constexpr int HALF = CONV_WARPS / 2;                              // converters of K^, and of V^
+    static_assert((LIFT || STAGES >= 2) && KB >= 2 && KB <= 6 && SMEM <= LIMIT, "shared memory");
+    static constexpr int SOFT0 = 4, CONV0 = SOFT0 + 4 * NT, CONV_WARPS = LIFT ? 0 : 8;  // first softmax / converter warp
+    static constexpr int HALF = CONV_WARPS / 2;                                         // converters of K^, and of V^
     static constexpr int WARPS = CONV0 + CONV_WARPS;
     static constexpr int THREADS = WARPS * 32;
 };
 
-// ---- workspace: [per CTA: the unit it starts in][pieces: m, l][pieces: o] ----
+// ---- workspace: [per CTA: the unit it starts in][pieces: m, l][pieces: o][lifted: info][lifted: operands] ----
 struct ChunkWork {
     int32_t *first;  // [CTAs][8]: sequence, head, unit, the unit's first step, its steps, span
     float *ml;       // [2 CTAs][ROWS][2]
     float *o;        // [2 CTAs][ROWS][D]
+    int4 *info;      // [lift_cap]: copied tiles, exponents of K^ and V^
+    uint8_t *image;  // [lift_cap][K^, V^]
+    int lift_cap;    // blocks that fit; 0: not lifted
 };
-inline ChunkWork chunk_work(void *ws, int ctas, int rows, int D, size_t *bytes) {
-    uint8_t *w = static_cast<uint8_t *>(ws);
-    const size_t head = (static_cast<size_t>(ctas) * 32 + 255) / 256 * 256, ml = static_cast<size_t>(2) * ctas * rows * 8;
-    if (bytes) *bytes = head + ml + static_cast<size_t>(2) * ctas * rows * D * 4;
-    return ChunkWork{reinterpret_cast<int32_t *>(w), reinterpret_cast<float *>(w + head), reinterpret_cast<float *>(w + head + ml)};
+constexpr size_t kLiftBytes = size_t(2) << 30;  // most that lifted operands may take
+
+// Blocks (of one KV head) that the chunk class of a call can have, all heads together; 0 if their operands
+// would pass kLiftBytes.
+inline long long lift_blocks(const PagedAttnParams &p, int D) {
+    const long long seqs = p.v.n_tokens / p.from_q < p.v.n_seqs ? p.v.n_tokens / p.from_q : p.v.n_seqs;
+    const long long per = p.v.max_len > 0 ? (static_cast<long long>(p.v.max_len) + kChunkKeys - 1) / kChunkKeys : 1;
+    const long long n = seqs * per * p.v.Hkv;
+    return n <= static_cast<long long>(kLiftBytes / (kChunkKeys * D * 4)) ? n : 0;
+}
+inline ChunkWork chunk_work(const PagedAttnParams &p, int ctas, int rows, int D, size_t *bytes) {
+    uint8_t *w = static_cast<uint8_t *>(p.workspace);
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    const size_t ml = up(static_cast<size_t>(ctas) * 32), o = ml + up(static_cast<size_t>(2) * ctas * rows * 8);
+    const size_t info = o + up(static_cast<size_t>(2) * ctas * rows * D * 4);
+    const long long cap = lift_blocks(p, D);
+    const size_t image = info + up(static_cast<size_t>(cap) * 16);
+    if (bytes) *bytes = image + static_cast<size_t>(cap) * kChunkKeys * D * 4;
+    return ChunkWork{reinterpret_cast<int32_t *>(w), reinterpret_cast<float *>(w + ml), reinterpret_cast<float *>(w + o),
+                     reinterpret_cast<int4 *>(w + info), w + image, static_cast<int>(cap)};
 }
 
 constexpr int kChunkMaxSeqs = 256;  // sequences of one launch (their prefix sums sit in shared memory)
@@ -196,11 +398,11 @@ struct ChunkSeq {
     int first, n, len, units;  // units per KV head
 };
 template <int ROWS>
-__device__ __forceinline__ ChunkSeq chunk_seq(const PagedView &v, int G, int min_q, int b) {
+__device__ __forceinline__ ChunkSeq chunk_seq(const PagedView &v, int G, int from_q, int b) {
     const PagedSeq s = paged_seq(v, b);
     ChunkSeq c;
     c.first = s.first;
-    c.n = s.n >= min_q ? s.n : 0;  // shorter ones belong to the split kernel
+    c.n = s.n >= from_q ? s.n : 0;  // shorter ones belong to the split kernel
     c.len = s.len;
     c.units = static_cast<int>((static_cast<long long>(c.n) * G + ROWS - 1) / ROWS);
     return c;
@@ -212,6 +414,83 @@ __device__ __forceinline__ int chunk_steps(const ChunkSeq &s, int G, int u) {
     return max(1, (last + NK) / NK);
 }
 
+// blocks of 64 positions of a sequence (at least one, as its units have)
+__device__ __forceinline__ int lift_blocks_of(const ChunkSeq &s) { return s.units > 0 ? max(1, (s.len + kChunkKeys - 1) / kChunkKeys) : 0; }
+
+// In place: a[0 .. n) (counts) to a[0 .. n] (sums of those before), by one warp.
+__device__ __forceinline__ void warp_prefix(int *a, int n) {
+    const int lane = threadIdx.x & 31;
+    int base = 0;
+    for (int b0 = 0; b0 < n; b0 += 32) {
+        const int own = b0 + lane < n ? a[b0 + lane] : 0;
+        int x = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (b0 + lane < n) a[b0 + lane] = base + x - own;
+        base += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) a[n] = base;
+}
+
+// The operands of every block of the sequences of the chunk class: one warp per (block, K^ or V^).
+constexpr int kLiftWarps = 8;
+template <int KT, int VT, int NS>
+__global__ void __launch_bounds__(32 * kLiftWarps) paged_lift_kernel(const PagedAttnParams p, const ChunkWork work) {
+    using C = ChunkCfg<KT, VT, NS, true>;
+    using T = typename C::T;
+    __shared__ int s_blocks[kChunkMaxSeqs + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const PagedView &v = p.v;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    for (int b = threadIdx.x; b < v.n_seqs; b += 32 * kLiftWarps)
+        s_blocks[b] = lift_blocks_of(chunk_seq<C::ROWS>(v, p.G, p.from_q, b)) * v.Hkv;
+    __syncthreads();
+    if (warp == 0) warp_prefix(s_blocks, v.n_seqs);
+    __syncthreads();
+    const int total = s_blocks[v.n_seqs];
+    for (int item = blockIdx.x * kLiftWarps + warp; item < 2 * total; item += gridDim.x * kLiftWarps) {
+        const int blk = item >> 1;
+        const bool keys = (item & 1) == 0;
+        int lo = 0, hi = v.n_seqs;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_blocks[mid] <= blk)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        if (s_blocks[lo + 1] > work.lift_cap) continue;  // left out of the chunk kernel, too
+        const ChunkSeq s = chunk_seq<C::ROWS>(v, p.G, p.from_q, lo);
+        const int per = lift_blocks_of(s), h = (blk - s_blocks[lo]) / per, kb = blk - s_blocks[lo] - h * per;
+        // lane i has the page of tile i
+        const int t = kb * C::TILES + (lane & (C::TILES - 1)), entry = t / v.page_tiles;
+        const int page = t * kTileRows < s.len ? __ldg(v.table + static_cast<size_t>(lo) * v.stride + entry) : -1;
+        const bool in = page >= 0 && page < v.n_pages;
+        if (keys && !in && t * kTileRows < s.len && lane < C::TILES) paged_error(v);
+        const BlockRows use{static_cast<int>(__ballot_sync(0xffffffffu, in) & ((1u << C::TILES) - 1u)), s.len - kb * C::NK};
+        // a tile without a page reads the pool's first record; its rows are not in use
+        const long long record = in ? (static_cast<long long>(page) * v.Hkv + h) * v.page_tiles + (t - entry * v.page_tiles) : 0;
+        auto tile = [&](int i) -> const uint8_t * {  // by the whole warp; i may differ between lanes
+            return v.pool + __shfl_sync(0xffffffffu, record, i) * T::BYTES;
+        };
+        uint8_t *image = work.image + static_cast<size_t>(blk) * C::IMAGE;
+        int32_t *info = reinterpret_cast<int32_t *>(work.info + blk);
+        if (keys) {
+            const int e = block_exp<KT, T::OFF_KS, NS>(tile, use);
+            if (lane == 0) info[0] = use.got, info[1] = e;
+            convert_keys<KT, VT, NS>(tile, image, e, 0, 1);
+        } else {
+            const int e = block_exp<VT, T::OFF_VS, NS>(tile, use);
+            if (lane == 0) info[2] = e;
+            convert_values<KT, VT, NS>(tile, image + C::KHAT, e, use, 0, 1);
+        }
+    }
+}
+
 // A walk over the units of a span: unit u of head h of sequence b, its steps, and the range of them
 // that belongs to this CTA.
 struct ChunkWalk {
@@ -219,17 +498,17 @@ struct ChunkWalk {
     int b, h, u, steps;
 };
 
-template <int KT, int VT, int NS, int DT>
-__global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
+template <int KT, int VT, int NS, int DT, bool LIFT>
+__global__ void __launch_bounds__(ChunkCfg<KT, VT, NS, LIFT>::THREADS, 1)
     paged_chunk_kernel(const PagedAttnParams p, const ChunkWork work) {
-    using C = ChunkCfg<KT, VT, NS>;
+    using C = ChunkCfg<KT, VT, NS, LIFT>;
     using T = typename C::T;
     using X = typename Act<DT>::type;
     constexpr int D = C::D, NK = C::NK, NT = C::NT, ROWS = C::ROWS;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t raw_full[4], raw_empty[4], k_ready[2], k_free[2], v_ready[2], v_free[2];
+    __shared__ __align__(8) uint64_t raw_full[4], raw_empty[4], k_ready[6], k_free[6], v_ready[6], v_free[6];
     __shared__ __align__(8) uint64_t s_ready[2], s_free[2], p_ready[2], pv_done[2], q_ready[2], drain[2];
-    __shared__ int s_pre[kChunkMaxSeqs + 1];
+    __shared__ int s_pre[kChunkMaxSeqs + 1], s_blocks[LIFT ? kChunkMaxSeqs + 1 : 1];
     __shared__ int s_start[4];                       // sequence, head, unit, step of this CTA's first step
     __shared__ int s_ok[8], s_exp[8][2];             // per block: copied tiles; exponents of K^ and V^
     __shared__ uint32_t s_tmem;
@@ -242,11 +521,15 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
             mbar_init(raw_full + i, 1);
             mbar_init(raw_empty + i, C::CONV_WARPS);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(k_ready + i, C::HALF);
+        for (int i = 0; i < C::KB; ++i) {
+            mbar_init(k_ready + i, LIFT ? 1 : C::HALF);
             mbar_init(k_free + i, NT);
-            mbar_init(v_ready + i, C::HALF);
+        }
+        for (int i = 0; i < C::VB; ++i) {
+            mbar_init(v_ready + i, LIFT ? 1 : C::HALF);
             mbar_init(v_free + i, NT);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(s_ready + i, 1);
             mbar_init(s_free + i, 4);
             mbar_init(p_ready + i, 4);
@@ -265,32 +548,31 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
     // ---- steps before each sequence, and where this CTA starts ----
+    if constexpr (LIFT) {
+        for (int b = threadIdx.x; b < v.n_seqs; b += C::THREADS)
+            s_blocks[b] = lift_blocks_of(chunk_seq<ROWS>(v, G, p.from_q, b)) * v.Hkv;
+        __syncthreads();
+        if (warp == 0) warp_prefix(s_blocks, v.n_seqs);
+        __syncthreads();
+    }
     for (int b = warp; b < v.n_seqs; b += C::WARPS) {
-        const ChunkSeq s = chunk_seq<ROWS>(v, G, p.split_below, b);
+        const ChunkSeq s = chunk_seq<ROWS>(v, G, p.from_q, b);
         int sum = 0;
         for (int u = lane; u < s.units; u += 32) sum += chunk_steps<ROWS, NK>(s, G, u);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) s_pre[b + 1] = sum * v.Hkv;
-        if (blockIdx.x == 0 && lane == 0 && !paged_seq(v, b).ok) paged_error(v);
+        bool ok = paged_seq(v, b).ok;
+        if (LIFT && s_blocks[b + 1] > work.lift_cap) {  // more tokens than the call has: offsets that overlap
+            ok = false;
+            sum = 0;
+        }
+        if (lane == 0) s_pre[b] = sum * v.Hkv;
+        if (blockIdx.x == 0 && lane == 0 && !ok) paged_error(v);
     }
     t5_fence_before();
     __syncthreads();
     t5_fence_after();
-    if (warp == 0) {
-        int base = 0;
-        if (lane == 0) s_pre[0] = 0;
-        for (int b0 = 0; b0 < v.n_seqs; b0 += 32) {
-            int x = b0 + lane < v.n_seqs ? s_pre[b0 + lane + 1] : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
-            }
-            if (b0 + lane < v.n_seqs) s_pre[b0 + lane + 1] = base + x;
-            base += __shfl_sync(0xffffffffu, x, 31);
-        }
-    }
+    if (warp == 0) warp_prefix(s_pre, v.n_seqs);
     __syncthreads();
     const int total = s_pre[v.n_seqs];
     // at least kMinSpan steps per CTA: shorter spans cost more in pieces than they gain
@@ -308,7 +590,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
             else
                 hi = mid;
         }
-        const ChunkSeq s = chunk_seq<ROWS>(v, G, p.split_below, lo);
+        const ChunkSeq s = chunk_seq<ROWS>(v, G, p.from_q, lo);
         const int per_head = (s_pre[lo + 1] - s_pre[lo]) / v.Hkv;
         int r = x0 - s_pre[lo];
         const int h = r / per_head;
@@ -346,7 +628,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
         w.b = s_start[0];
         w.h = s_start[1];
         w.u = s_start[2];
-        w.s = chunk_seq<ROWS>(v, G, p.split_below, w.b);
+        w.s = chunk_seq<ROWS>(v, G, p.from_q, w.b);
         w.steps = chunk_steps<ROWS, NK>(w.s, G, w.u);
         return w;
     };
@@ -357,7 +639,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
                 w.h = 0;
                 ++w.b;
                 while (s_pre[w.b + 1] == s_pre[w.b]) ++w.b;
-                w.s = chunk_seq<ROWS>(v, G, p.split_below, w.b);
+                w.s = chunk_seq<ROWS>(v, G, p.from_q, w.b);
             }
         }
         w.steps = chunk_steps<ROWS, NK>(w.s, G, w.u);
@@ -369,8 +651,59 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
     };
 
     if (NX > 0) {
-        if (warp == 0) {
-            // ---------------- copies ----------------
+        if (LIFT && warp == 0) {
+            // ---------------- copies of lifted operands ----------------
+            ChunkWalk w = begin();
+            int t = s_start[3], issued = 0;
+            bool ok = true;
+            int4 info = make_int4(0, 0, 0, 0);
+            size_t blk = 0;
+            auto look_up = [&]() {  // a step ahead
+                blk = static_cast<size_t>(s_blocks[w.b] + w.h * lift_blocks_of(w.s) + t);
+                info = __ldcg(work.info + blk);
+            };
+            look_up();
+            for (int x = 0; x < NX; ++x) {
+                const int buf = x % C::KB, use = x / C::KB;
+                if (use > 0) ok = __all_sync(0xffffffffu, paged_wait(k_free + buf, (use - 1) & 1));
+                if (!ok) break;
+                const uint8_t *src = work.image + blk * C::IMAGE;
+                if (lane == 0) {
+                    s_ok[x & 7] = info.x;
+                    s_exp[x & 7][0] = info.y;
+                    s_exp[x & 7][1] = info.z;
+                }
+                __syncwarp();
+                if (t5_elect()) {
+                    mbar_arrive_expect_tx(k_ready + buf, C::KHAT);
+                    bulk_g2s(smem + C::OFF_K + buf * C::KHAT, src, C::KHAT, k_ready + buf);
+                }
+                __syncwarp();
+                if (use > 0) ok = __all_sync(0xffffffffu, paged_wait(v_free + buf, (use - 1) & 1));
+                if (ok && t5_elect()) {
+                    mbar_arrive_expect_tx(v_ready + buf, C::VHAT);
+                    bulk_g2s(smem + C::OFF_V + buf * C::VHAT, src + C::KHAT, C::VHAT, v_ready + buf);
+                }
+                __syncwarp();
+                issued = x + 1;
+                if (!ok) break;
+                if (x + 1 < NX) {
+                    if (++t == w.steps) {
+                        advance(w);
+                        t = 0;
+                    }
+                    look_up();
+                }
+            }
+            if (!ok && lane == 0) atomicOr(v.err, KVQ_DEVERR_TIMEOUT);
+            for (int i = 0; i < C::KB; ++i)  // every copy lands before the memory is freed
+                if (i < issued) {
+                    (void)paged_wait(k_ready + i, ((issued - 1 - i) / C::KB) & 1);
+                    (void)paged_wait(v_ready + i, ((issued - 1 - i) / C::KB) & 1);
+                }
+            __syncwarp();
+        } else if (!LIFT && warp == 0) {
+            // ---------------- copies of raw tiles ----------------
             // lane i < 4 has tile i of the block; its page number is looked up one step ahead
             ChunkWalk w = begin();
             int t = s_start[3], issued = 0, page = -1, tile = 0, tiles = 0;
@@ -384,7 +717,8 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
             look_up();
             bool ok = true;
             for (int x = 0; x < NX; ++x) {
-                const int st = x % C::STAGES, use = x / C::STAGES;
+                constexpr int STAGES = LIFT ? 1 : C::STAGES;
+                const int st = x % STAGES, use = x / STAGES;
                 if (use > 0) ok = __all_sync(0xffffffffu, paged_wait(raw_empty + st, (use - 1) & 1));
                 if (!ok) break;
                 const bool in = page >= 0 && page < v.n_pages;
@@ -413,7 +747,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
             }
             if (!ok && lane == 0) atomicOr(v.err, KVQ_DEVERR_TIMEOUT);
             for (int i = 0; i < C::STAGES; ++i)  // every copy lands before the memory is freed
-                if (i < issued) (void)paged_wait(raw_full + i, ((issued - 1 - i) / C::STAGES) & 1);
+                if (i < issued) (void)paged_wait(raw_full + i, ((issued - 1 - i) / (LIFT ? 1 : C::STAGES)) & 1);
             __syncwarp();
         } else if (warp == 1 || warp == 2) {
             // ---------------- MMA issue ----------------
@@ -500,184 +834,35 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS>::THREADS, 1)
             if (t5_elect()) t5_commit(drain + warp - 1);
             __syncwarp();
             (void)paged_wait(drain + warp - 1, 0);
-        } else if (warp >= C::CONV0) {
+        } else if (!LIFT && warp >= C::CONV0) {
             // ---------------- converters: codes -> K^ (first half of the warps), V^ (second half) ----------------
             const bool keys = warp < C::CONV0 + C::HALF;
             const int cw = warp - C::CONV0 - (keys ? 0 : C::HALF);
-            const uint32_t magic = 0x64006400u;  // f16 1024 | bits = 1024 + bits
-            const __half2 k1032 = __float2half2_rn(1032.0f), k16th = __float2half2_rn(0.0625f), km72 = __float2half2_rn(-72.0f);
-            const __half2 k2to14 = __float2half2_rn(16384.0f);
-            // bytes 0, 2 / 1, 3 of a word of q8_0 codes, times 2^-10: f16 subnormals times 2^14, exact
-            auto q8_02 = [&](uint32_t w) { return __hmul2(u32_as_h2(perm(w, 0u, 0xA280u) & 0x807f807fu), k2to14); };
-            auto q8_13 = [&](uint32_t w) { return __hmul2(u32_as_h2(perm(w, 0u, 0xB391u) & 0x807f807fu), k2to14); };
-            // bytes 0, 2 of a word of q4_0 codes: low or high nibbles less 8
-            auto q4lo = [&](uint32_t x) { return __hsub2(u32_as_h2((x & 0x000f000fu) | magic), k1032); };
-            auto q4hi = [&](uint32_t x) { return __hfma2(u32_as_h2((x & 0x00f000f0u) | magic), k16th, km72); };
-            auto both = [](uint32_t w, int upper) { return perm(w, 0u, upper ? 0x3232u : 0x1010u); };  // one half twice
-            // rows of tile i of the block in use
-            auto rows_of = [&](int len, int t, int got, int i) {
-                return ((got >> i) & 1) ? max(0, min(kTileRows, len - (t * C::TILES + i) * kTileRows)) : 0;
-            };
-            // Exponent e >= 0 with |value| 2^-e below 2^14 (q4_0) or 2^12 (q8_0, whose scale meets codes times
-            // 2^-10) over the block's rows in use; at most 11.
-            auto block_exp = [&](const uint8_t *sc, int type, int len, int t, int got) {
-                const float cmax = type == KVQ_Q8_0 ? 127.f : 8.f;
-                const int most = type == KVQ_Q8_0 ? 12 : 14;
-                uint32_t m = 0;
-#pragma unroll
-                for (int k = 0; k < NS; ++k) {
-                    const int gi = k * 32 + lane, i = gi / (8 * NS), in = gi % (8 * NS);  // tile, 16-byte group of its scales
-                    uint4 w = *reinterpret_cast<const uint4 *>(sc + i * T::BYTES + in * 16);
-                    const int use = rows_of(len, t, got, i), ka = 2 * ((in & 7) >> 1);
-                    if (use < kTileRows) {
-                        keep_branch();
-                        auto cut = [&](uint32_t x, int r) { return r >= use ? 0u : (r + 1 >= use ? (x & 0xffffu) : x); };
-                        w = make_uint4(cut(w.x, ka), cut(w.y, ka + 8), cut(w.z, ka), cut(w.w, ka + 8));
-                    }
-                    const __half2 a = __hmax2(__habs2(u32_as_h2(w.x)), __habs2(u32_as_h2(w.y)));
-                    const __half2 b = __hmax2(__habs2(u32_as_h2(w.z)), __habs2(u32_as_h2(w.w)));
-                    m = h2_as_u32(__hmax2(u32_as_h2(m), __hmax2(a, b)));
-                }
-                const float2 f = __half22float2(u32_as_h2(m));
-                float top = fmaxf(f.x, f.y) * cmax;
-                if (!__any_sync(0xffffffffu, top > static_cast<float>(1 << most))) return 0;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                return min(11, max(0, ilogbf(top) - (most - 1)));
-            };
-            auto pow2 = [](int e) { return __int_as_float((127 + e) << 23); };
-
             ChunkWalk w = begin();
             int t = s_start[3];
             bool ok = true;
             for (int x = 0; x < NX && ok; ++x) {
-                const int sg = x % C::STAGES;
+                constexpr int STAGES = LIFT ? 1 : C::STAGES, HALF = LIFT ? 1 : C::HALF;
+                const int sg = x % STAGES;
                 const uint8_t *st = smem + sg * C::STAGE;
-                ok = paged_wait(raw_full + sg, (x / C::STAGES) & 1);
+                ok = paged_wait(raw_full + sg, (x / STAGES) & 1);
                 const int buf = keys ? x % C::KB : x % C::VB, use_no = keys ? x / C::KB : x / C::VB;
                 if (use_no > 0) ok = paged_wait((keys ? k_free : v_free) + buf, (use_no - 1) & 1) && ok;
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                const int got = s_ok[x & 7], len = w.s.len;
+                const BlockRows use{s_ok[x & 7], w.s.len - t * NK};
+                auto tile = [&](int i) { return st + i * T::BYTES; };
                 if (keys) {
-                    // ---- K^: rows past the sequence's end may become anything; their scores are masked ----
-                    int e = 0;
-                    if constexpr (KT != KVQ_F16) e = block_exp(st + T::OFF_KS, KT, len, t, got);
+                    const int e = block_exp<KT, T::OFF_KS, NS>(tile, use);
                     if (cw == 0 && lane == 0) s_exp[x & 7][0] = e;
                     if (cw == 1) {  // the softmax warps need V^'s exponent with S, perhaps before V^ is made
-                        int ev = 0;
-                        if constexpr (VT != KVQ_F16) ev = block_exp(st + T::OFF_VS, VT, len, t, got);
+                        const int ev = block_exp<VT, T::OFF_VS, NS>(tile, use);
                         if (lane == 0) s_exp[x & 7][1] = ev;
                     }
-                    uint8_t *kh = smem + C::OFF_K + buf * C::KHAT;
-                    const __half2 fk = __float2half2_rn(pow2(KT == KVQ_Q8_0 ? 10 - e : -e));
-                    const int n = lane >> 2, jd = lane & 3;  // key n (and n + 8) of the tile, 4-value group jd
-                    uint8_t *lane_at = kh + (jd >> 1) * 128 + n * 16 + (jd & 1) * 8;  // core_at(n, 4 jd, D)
-                    auto put = [&](int at, __half2 c02, __half2 c13, __half2 d2) {
-                        *reinterpret_cast<uint2 *>(lane_at + at) = make_uint2(h2_as_u32(__hmul2(c02, d2)), h2_as_u32(__hmul2(c13, d2)));
-                    };
-                    // core_at(16 i + n + 8 s, dim + 4 jd, D) less lane_at, for dim a multiple of 16
-                    auto at = [](int i, int s8, int dim) { return (2 * i + s8) * (D * 16) + dim * 16; };
-                    if constexpr (KT == KVQ_Q8_0) {
-#pragma unroll 4
-                        for (int wu = cw; wu < C::TILES * NS * 4; wu += C::HALF) {
-                            const int ts = wu >> 2, b = wu & 3, i = ts / NS, sl = ts % NS, dim = sl * kSlice + 32 * b;
-                            const uint8_t *tile = st + i * T::BYTES;
-                            const uint4 c = *reinterpret_cast<const uint4 *>(tile + sl * 2048 + (b * 32 + lane) * 16);
-                            const uint2 sc = *reinterpret_cast<const uint2 *>(tile + T::OFF_KS + sl * kScaleTile + (n >> 1) * 32 + b * 8);
-                            const __half2 da = __hmul2(u32_as_h2(both(sc.x, n & 1)), fk), db = __hmul2(u32_as_h2(both(sc.y, n & 1)), fk);
-                            put(at(i, 0, dim), q8_02(c.x), q8_13(c.x), da);
-                            put(at(i, 0, dim + 16), q8_02(c.y), q8_13(c.y), da);
-                            put(at(i, 1, dim), q8_02(c.z), q8_13(c.z), db);
-                            put(at(i, 1, dim + 16), q8_02(c.w), q8_13(c.w), db);
-                        }
-                    } else if constexpr (KT == KVQ_Q4_0) {
-#pragma unroll 2
-                        for (int wu = cw; wu < C::TILES * NS * 2; wu += C::HALF) {
-                            const int ts = wu >> 1, b2 = wu & 1, i = ts / NS, sl = ts % NS;
-                            const uint8_t *tile = st + i * T::BYTES;
-                            const uint4 c = *reinterpret_cast<const uint4 *>(tile + sl * 1024 + (b2 * 32 + lane) * 16);
-                            const uint4 sc = *reinterpret_cast<const uint4 *>(tile + T::OFF_KS + sl * kScaleTile + (n >> 1) * 32 + b2 * 16);
-                            const uint32_t cs[4] = {c.x, c.y, c.z, c.w}, ss[4] = {sc.x, sc.y, sc.z, sc.w};
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {  // block 2 b2 + q / 2, key n + 8 (q % 2)
-                                const int dim = sl * kSlice + 64 * b2 + 32 * (q >> 1);
-                                const __half2 d2 = __hmul2(u32_as_h2(both(ss[q], n & 1)), fk);
-                                const uint32_t odd = cs[q] >> 8;
-                                put(at(i, q & 1, dim), q4lo(cs[q]), q4lo(odd), d2);
-                                put(at(i, q & 1, dim + 16), q4hi(cs[q]), q4hi(odd), d2);
-                            }
-                        }
-                    } else {
-#pragma unroll 4
-                        for (int wu = cw; wu < C::TILES * NS * 8; wu += C::HALF) {
-                            const int ts = wu >> 3, ch = wu & 7, i = ts / NS, sl = ts % NS, dim = sl * kSlice + 32 * (ch >> 1);
-                            const uint4 c = *reinterpret_cast<const uint4 *>(st + i * T::BYTES + sl * 4096 + (ch * 32 + lane) * 16);
-                            *reinterpret_cast<uint2 *>(lane_at + at(i, ch & 1, dim)) = make_uint2(c.x, c.y);
-                            *reinterpret_cast<uint2 *>(lane_at + at(i, ch & 1, dim + 16)) = make_uint2(c.z, c.w);
-                        }
-                    }
+                    convert_keys<KT, VT, NS>(tile, smem + C::OFF_K + buf * C::KHAT, e, cw, HALF);
                 } else {
-                    // ---- V^: rows past the sequence's end may hold any bits and become 0 ----
-                    int e = 0;
-                    if constexpr (VT != KVQ_F16) e = block_exp(st + T::OFF_VS, VT, len, t, got);
-                    uint8_t *vh = smem + C::OFF_V + buf * C::VHAT;
-                    const __half2 fv = __float2half2_rn(pow2(VT == KVQ_Q8_0 ? 10 - e : -e));
-                    const int np = lane >> 2, j = lane & 3;
-                    uint8_t *lane_at = vh + np * 16 + j * 4;  // row np of a core matrix, keys 2j, 2j + 1
-                    // value dim + 2 np + odd of keys 16 i + 2j, + 1 (and + 8, + 9): row (dim / 8 + odd) * 8 + np
-                    auto at = [](int i, int dim, int odd) { return ((dim >> 3) + odd) * (NK * 16) + 2 * i * 128; };
-                    auto put = [&](int a, __half2 ca, __half2 cb, __half2 da, __half2 db) {
-                        *reinterpret_cast<uint32_t *>(lane_at + a) = h2_as_u32(__hmul2(ca, da));
-                        *reinterpret_cast<uint32_t *>(lane_at + a + 128) = h2_as_u32(__hmul2(cb, db));
-                    };
-                    auto cut = [&](uint32_t s2, int r, int use) { return r >= use ? 0u : (r + 1 >= use ? (s2 & 0xffffu) : s2); };
-                    if constexpr (VT == KVQ_Q8_0) {
-#pragma unroll 4
-                        for (int wu = cw; wu < C::TILES * NS * 4; wu += C::HALF) {
-                            const int ts = wu >> 2, b = wu & 3, i = ts / NS, sl = ts % NS;
-                            const uint8_t *tile = st + i * T::BYTES;
-                            const uint4 c = *reinterpret_cast<const uint4 *>(tile + T::OFF_V + sl * 2048 + (b * 32 + lane) * 16);
-                            const uint2 sc = *reinterpret_cast<const uint2 *>(tile + T::OFF_VS + sl * kScaleTile + j * 32 + b * 8);
-                            const int use = rows_of(len, t, got, i);
-                            const __half2 da = __hmul2(u32_as_h2(cut(sc.x, 2 * j, use)), fv), db = __hmul2(u32_as_h2(cut(sc.y, 2 * j + 8, use)), fv);
-                            const uint32_t cs[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) put(at(i, sl * kSlice + 32 * b + 16 * (q >> 1), q & 1), q8_02(cs[q]), q8_13(cs[q]), da, db);
-                        }
-                    } else if constexpr (VT == KVQ_Q4_0) {
-#pragma unroll 2
-                        for (int wu = cw; wu < C::TILES * NS * 2; wu += C::HALF) {
-                            const int ts = wu >> 1, b2 = wu & 1, i = ts / NS, sl = ts % NS;
-                            const uint8_t *tile = st + i * T::BYTES;
-                            const uint4 c = *reinterpret_cast<const uint4 *>(tile + T::OFF_V + sl * 1024 + (b2 * 32 + lane) * 16);
-                            const uint4 sc = *reinterpret_cast<const uint4 *>(tile + T::OFF_VS + sl * kScaleTile + j * 32 + b2 * 16);
-                            const int use = rows_of(len, t, got, i);
-                            const __half2 d[4] = {__hmul2(u32_as_h2(cut(sc.x, 2 * j, use)), fv), __hmul2(u32_as_h2(cut(sc.y, 2 * j + 8, use)), fv),
-                                                  __hmul2(u32_as_h2(cut(sc.z, 2 * j, use)), fv), __hmul2(u32_as_h2(cut(sc.w, 2 * j + 8, use)), fv)};
-                            const uint32_t cs[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {  // block 2 b2 + q / 2, value 2 np + q % 2 (and + 16)
-                                const int dim = sl * kSlice + 64 * b2 + 32 * (q >> 1);
-                                const uint32_t odd = cs[q] >> 8;
-                                put(at(i, dim, q & 1), q4lo(cs[q]), q4lo(odd), d[2 * (q >> 1)], d[2 * (q >> 1) + 1]);
-                                put(at(i, dim + 16, q & 1), q4hi(cs[q]), q4hi(odd), d[2 * (q >> 1)], d[2 * (q >> 1) + 1]);
-                            }
-                        }
-                    } else {
-#pragma unroll 4
-                        for (int wu = cw; wu < C::TILES * NS * 8; wu += C::HALF) {
-                            const int ts = wu >> 3, ch = wu & 7, i = ts / NS, sl = ts % NS;
-                            const uint4 c = *reinterpret_cast<const uint4 *>(st + i * T::BYTES + T::OFF_V + sl * 4096 + (ch * 32 + lane) * 16);
-                            const int use = rows_of(len, t, got, i), dim = sl * kSlice + 32 * (ch >> 1) + 16 * (ch & 1);
-#pragma unroll
-                            for (int odd = 0; odd < 2; ++odd) {
-                                uint8_t *to = lane_at + at(i, dim, odd);
-                                *reinterpret_cast<uint32_t *>(to) = cut(odd ? c.z : c.x, 2 * j, use);
-                                *reinterpret_cast<uint32_t *>(to + 128) = cut(odd ? c.w : c.y, 2 * j + 8, use);
-                            }
-                        }
-                    }
+                    const int e = block_exp<VT, T::OFF_VS, NS>(tile, use);
+                    convert_values<KT, VT, NS>(tile, smem + C::OFF_V + buf * C::VHAT, e, use, cw, HALF);
                 }
                 smem_to_async();
                 __syncwarp();
@@ -968,19 +1153,19 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-template <int KT, int VT, int NS, int DT>
+template <int KT, int VT, int NS, int DT, bool LIFT>
 cudaError_t launch_chunk_t(const PagedAttnParams &p, cudaStream_t stream) {
-    using C = ChunkCfg<KT, VT, NS>;
+    using C = ChunkCfg<KT, VT, NS, LIFT>;
     static bool configured[kPagedMaxDevices] = {};
     int dev = 0, sms = 0;
     cudaError_t e = paged_device(&dev, &sms);
     if (e != cudaSuccess) return e;
     if (!configured[dev]) {
-        e = cudaFuncSetAttribute(paged_chunk_kernel<KT, VT, NS, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        e = cudaFuncSetAttribute(paged_chunk_kernel<KT, VT, NS, DT, LIFT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
-    const ChunkWork work = chunk_work(p.workspace, sms, C::ROWS, C::D, nullptr);
+    const ChunkWork work = chunk_work(p, sms, C::ROWS, C::D, nullptr);
     // sequences of one launch: their prefix sums fit shared memory, their steps 2^30
     const long long units = (static_cast<long long>(p.v.max_q) * p.G + C::ROWS - 1) / C::ROWS;
     const long long per_seq = units * ((p.v.max_len + C::NK) / C::NK) * p.v.Hkv;
@@ -989,7 +1174,11 @@ cudaError_t launch_chunk_t(const PagedAttnParams &p, cudaStream_t stream) {
     if (most < 1) return cudaErrorInvalidValue;
     for (int b = 0; b < p.v.n_seqs; b += most) {
         const PagedAttnParams q = paged_some(p, b, most);
-        e = launch_dependent(paged_chunk_kernel<KT, VT, NS, DT>, dim3(sms), C::THREADS, C::SMEM, stream, q, work);
+        if (LIFT) {
+            e = launch_dependent(paged_lift_kernel<KT, VT, NS>, dim3(sms * 4), 32 * kLiftWarps, 0, stream, q, work);
+            if (e != cudaSuccess) return e;
+        }
+        e = launch_dependent(paged_chunk_kernel<KT, VT, NS, DT, LIFT>, dim3(sms), C::THREADS, C::SMEM, stream, q, work);
         if (e != cudaSuccess) return e;
         if (sms == 1) continue;
         e = launch_dependent(paged_chunk_merge<NS, DT>, dim3(sms - 1, C::ROWS / 8), 256, 0, stream, q, work, static_cast<int>(C::ROWS));
@@ -1000,10 +1189,11 @@ cudaError_t launch_chunk_t(const PagedAttnParams &p, cudaStream_t stream) {
 
 template <int DT>
 cudaError_t launch_chunk_dt(int type_k, int type_v, int D, const PagedAttnParams &p, cudaStream_t s) {
+    const bool lift = lift_blocks(p, D) > 0;
 #define KVQ_CHUNK_CASE(KT_, VT_)                                                  \
-    if (type_k == KT_ && type_v == VT_) {                                         \
-        if (D == kSlice) return launch_chunk_t<KT_, VT_, 1, DT>(p, s);            \
-        if (D == 2 * kSlice) return launch_chunk_t<KT_, VT_, 2, DT>(p, s);        \
+    if (type_k == KT_ && type_v == VT_) {                                                            \
+        if (D == kSlice) return lift ? launch_chunk_t<KT_, VT_, 1, DT, true>(p, s) : launch_chunk_t<KT_, VT_, 1, DT, false>(p, s);     \
+        if (D == 2 * kSlice) return lift ? launch_chunk_t<KT_, VT_, 2, DT, true>(p, s) : launch_chunk_t<KT_, VT_, 2, DT, false>(p, s); \
     }
     KVQ_CHUNK_CASE(KVQ_F16, KVQ_F16)
     KVQ_CHUNK_CASE(KVQ_Q8_0, KVQ_Q8_0)

@@ -7,11 +7,11 @@ cudaError_t launch_paged_chunk_f16(int type_k, int type_v, int D, const PagedAtt
     return launch_chunk_dt<KVQ_DT_F16>(type_k, type_v, D, p, s);
 }
 
-cudaError_t paged_chunk_workspace(int D, size_t *bytes) {
+cudaError_t paged_chunk_workspace(int D, const PagedAttnParams &p, size_t *bytes) {
     int dev = 0, sms = 0;
     const cudaError_t e = paged_device(&dev, &sms);
     if (e != cudaSuccess) return e;
-    (void)chunk_work(nullptr, sms, D == kSlice ? ChunkCfg<KVQ_F16, KVQ_F16, 1>::ROWS : ChunkCfg<KVQ_F16, KVQ_F16, 2>::ROWS, D, bytes);
+    (void)chunk_work(p, sms, D == kSlice ? ChunkCfg<KVQ_F16, KVQ_F16, 1, true>::ROWS : ChunkCfg<KVQ_F16, KVQ_F16, 2, true>::ROWS, D, bytes);
     return cudaSuccess;
 }
 

@@ -347,7 +347,7 @@ struct Walk {
 // sequence b, without tokens if it belongs to the chunk kernel
 __device__ __forceinline__ PagedSeq split_seq(const PagedAttnParams &p, int b) {
     PagedSeq s = paged_seq(p.v, b);
-    if (s.n >= p.split_below) s.n = 0;
+    if (s.n >= p.from_q) s.n = 0;
     return s;
 }
 template <int TPS>
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
             for (int b = b0; b < b1; ++b) {
                 PagedSeq q = paged_seq(v, b);
                 if (blockIdx.x == 0 && !q.ok) paged_error(v);
-                if (q.n >= p.split_below) q.n = 0;
+                if (q.n >= p.from_q) q.n = 0;
                 const int tiles = (q.len + kTileRows - 1) / kTileRows, groups = (q.n * p.G + kRows - 1) / kRows;
                 shape[b] = make_int2(tiles, groups);
                 pre[b] = sum;
@@ -1013,7 +1013,7 @@ cudaError_t launch_split_t(const PagedAttnParams &p, cudaStream_t stream) {
         configured[dev] = true;
     }
     const SplitWork work = split_work(p.workspace, 2 * kSplitMaxWarps * sms);
-    const int max_q = p.v.max_q < p.split_below ? p.v.max_q : p.split_below - 1;
+    const int max_q = p.v.max_q < p.from_q ? p.v.max_q : p.from_q - 1;
     const int max_groups = static_cast<int>((static_cast<long long>(max_q) * p.G + kRows - 1) / kRows);
     // sequences of one launch: their prefix sums fit shared memory, their steps 2^30
     const long long per_seq = static_cast<long long>(p.v.max_len + kTileRows - 1) / kTileRows * p.v.Hkv * max_groups;
