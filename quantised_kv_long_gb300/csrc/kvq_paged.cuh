@@ -79,18 +79,21 @@ __device__ __forceinline__ uint8_t *paged_tile(const PagedView &v, int b, int h,
 
 // Bounded wait for a barrier phase: false after about two seconds.  The hardware holds the warp for up
 // to 20 us per try, so that a waiting warp takes few issue slots from the working ones.
+__device__ __forceinline__ bool paged_try(uint32_t addr, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(ok)
+                 : "r"(addr), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ bool paged_wait(uint64_t *bar, uint32_t parity) {
     const uint32_t addr = smem_u32(bar);
+    if (paged_try(addr, parity)) return true;
     const long long t0 = clock64();
-    while (true) {
-        uint32_t ok;
-        asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n selp.u32 %0, 1, 0, p;\n}\n"
-                     : "=r"(ok)
-                     : "r"(addr), "r"(parity)
-                     : "memory");
-        if (ok) return true;
+    while (!paged_try(addr, parity))
         if (clock64() - t0 > kWaitCycles) return false;
-    }
+    return true;
 }
 
 // At the head of a rarely taken branch: keeps the compiler from turning the branch into selects that every
@@ -110,8 +113,8 @@ struct Act<KVQ_DT_F32> {
 template <>
 struct Act<KVQ_DT_F16> {
     using type = __half;
-    static __device__ __forceinline__ float4 load4(const __half *p) {
-        const uint2 w = *reinterpret_cast<const uint2 *>(p);
+    static __device__ __forceinline__ float4 load4(const __half *p) { return widen(*reinterpret_cast<const uint2 *>(p)); }
+    static __device__ __forceinline__ float4 widen(uint2 w) {  // four values, as loaded
         const float2 a = __half22float2(u32_as_h2(w.x)), b = __half22float2(u32_as_h2(w.y));
         return make_float4(a.x, a.y, b.x, b.y);
     }
@@ -126,8 +129,8 @@ struct Act<KVQ_DT_F16> {
 template <>
 struct Act<KVQ_DT_BF16> {
     using type = __nv_bfloat16;
-    static __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-        const uint2 w = *reinterpret_cast<const uint2 *>(p);  // a bf16 is the upper half of an fp32
+    static __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) { return widen(*reinterpret_cast<const uint2 *>(p)); }
+    static __device__ __forceinline__ float4 widen(uint2 w) {  // a bf16 is the upper half of an fp32
         return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
                            __uint_as_float(w.y & 0xffff0000u));
     }

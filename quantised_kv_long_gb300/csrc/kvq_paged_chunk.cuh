@@ -11,8 +11,8 @@
 //
 // A step, by warps: warp 0 streams the block's tile records into a ring; half of the converter warps
 // turn key codes into the f16 operand K^ (keys x D) in shared memory, the other half value codes into
-// V^ (D x keys), once for all rows of the unit; warps 1 and 2 issue S = Q K^T and O += P V^ (one per
-// tile, or one per product where there is one tile); four warps per tile hold one row per thread:
+// V^ (D x keys), once for all rows of the unit; warp 1 issues S = Q K^T, warps 2 and 3 issue
+// O += P V^ of a tile each; four warps per tile hold one row per thread:
 // running maximum, weights, P into tensor memory, and the rescale of O when the maximum moves by more
 // than kChunkDrift.  S of the next block is computed while the softmax of this one runs (S and P have
 // their own columns).
@@ -26,7 +26,7 @@
 // word come out), and the rows of V^ (columns of O) in the order 0, 2, .., 14, 1, 3, .., 15 within each
 // sixteen, so that a warp's stores of V^ fill whole core matrices; the epilogue puts them back.
 //
-// Rounding.  Q is f16 after scaling each row by a power of two (exact for f16 and for bf16 in range).
+// Rounding.  Q is f16; a bf16 row outside f16's range is moved by a power of two.
 // K^ and V^ are scale x code rounded once to f16 (2^-11), P is f16 (2^-11); S, O, the maxima and
 // sums are fp32.  The output has 16 bits (2^-11 or 2^-8).  A block with scales that would leave f16
 // is stored times 2^-e, and S or P is multiplied by 2^e, both exact.
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS, LIFT>::THREADS, 1)
     constexpr int D = C::D, NK = C::NK, NT = C::NT, ROWS = C::ROWS;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t raw_full[4], raw_empty[4], k_ready[6], k_free[6], v_ready[6], v_free[6];
-    __shared__ __align__(8) uint64_t s_ready[2], s_free[2], p_ready[2], pv_done[2], q_ready[2], drain[2];
+    __shared__ __align__(8) uint64_t s_ready[2], s_free[2], p_ready[2], pv_done[2], q_ready[2], drain[3];
     __shared__ int s_pre[kChunkMaxSeqs + 1], s_blocks[LIFT ? kChunkMaxSeqs + 1 : 1];
     __shared__ int s_start[4];                       // sequence, head, unit, step of this CTA's first step
     __shared__ int s_ok[8], s_exp[8][2];             // per block: copied tiles; exponents of K^ and V^
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS, LIFT>::THREADS, 1)
         }
         for (int i = 0; i < C::KB; ++i) {
             mbar_init(k_ready + i, LIFT ? 1 : C::HALF);
-            mbar_init(k_free + i, NT);
+            mbar_init(k_free + i, 1);
         }
         for (int i = 0; i < C::VB; ++i) {
             mbar_init(v_ready + i, LIFT ? 1 : C::HALF);
@@ -536,8 +536,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS, LIFT>::THREADS, 1)
             mbar_init(pv_done + i, 1);
             mbar_init(q_ready + i, 4);
         }
-        mbar_init(drain, 1);
-        mbar_init(drain + 1, 1);
+        for (int i = 0; i < 3; ++i) mbar_init(drain + i, 1);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -749,85 +748,101 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS, LIFT>::THREADS, 1)
             for (int i = 0; i < C::STAGES; ++i)  // every copy lands before the memory is freed
                 if (i < issued) (void)paged_wait(raw_full + i, ((issued - 1 - i) / (LIFT ? 1 : C::STAGES)) & 1);
             __syncwarp();
-        } else if (warp == 1 || warp == 2) {
-            // ---------------- MMA issue ----------------
+        } else if (warp < C::SOFT0) {
+            // ---------------- MMA issue: warp 1 S = Q K^T of every tile, warps 2 and 3 O += P V^ of one ----------------
+            // A step costs each of these warps about 100 cycles per wait besides the MMAs, so the products that
+            // wait for the softmax have their own streams.
+            if (warp == 3 && lane == 0) {  // for the merge: the unit that this CTA starts in
+                const ChunkWalk w = begin();
+                int32_t *e = work.first + 8 * blockIdx.x;
+                e[0] = w.b;
+                e[1] = w.h;
+                e[2] = w.u;
+                e[3] = x0 - s_start[3];  // its first step
+                e[4] = w.steps;
+                e[5] = span;
+            }
+            __syncwarp();
             constexpr uint32_t ID_S = t5_idesc(C::M, NK), ID_O = t5_idesc(C::M, D);
-            const uint64_t qd = t5_desc(smem_u32(smem + C::OFF_Q), 128, D * 16);
-            const uint64_t kd = t5_desc(smem_u32(smem + C::OFF_K), 128, D * 16), vd = t5_desc(smem_u32(smem + C::OFF_V), 128, NK * 16);
-            const int tile = NT == 2 ? warp - 1 : 0;
-            auto qk = [&](int x) {  // S = Q K^(x)^T of this warp's tile
-                const uint64_t b = t5_plus(kd, (x % C::KB) * C::KHAT);
-                if (t5_elect()) {
-                    if (NT == 1 || tile == 0) {
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k) t5_mma_ts(tm + C::T_S, tm + C::T_Q + 8 * k, b + 16 * k, ID_S, k > 0);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k) t5_mma_ss(tm + C::T_S + NK, qd + 16 * k, b + 16 * k, ID_S, k > 0);
-                    }
-                    t5_commit(s_ready + tile);
-                    t5_commit(k_free + x % C::KB);
-                }
-                __syncwarp();
-            };
-            auto pv = [&](int x, bool start) {  // O += P V^(x)
-                const uint64_t b = t5_plus(vd, (x % C::VB) * C::VHAT);
-                const uint32_t o = t5_uniform(tm + C::T_O + tile * D), a = t5_uniform(tm + C::T_P + tile * (NK / 2));
-                const uint32_t add = t5_uniform(start ? 0u : 1u);
-                if (t5_elect()) {
-#pragma unroll
-                    for (int k = 0; k < NK / 16; ++k) t5_mma_ts(o, a + 8 * k, b + 16 * k, ID_O, k > 0 ? 1u : add);
-                    t5_commit(pv_done + tile);
-                    t5_commit(v_free + x % C::VB);
-                }
-                __syncwarp();
-            };
-            ChunkWalk w = begin();
-            int c0 = s_start[3], x = 0, done = 0, segs = 0;  // done, segs: steps and segments of the tile (barrier phases)
-            bool ok = true;
             auto wait = [&](uint64_t *bar, int phase) {
-                const bool got = __all_sync(0xffffffffu, paged_wait(bar, phase & 1)) != 0;
+                const bool got = __all_sync(0xffffffffu, paged_wait(bar, phase)) != 0;
                 t5_fence_after();
                 return got;
             };
-            auto k_wait = [&](int y) { return wait(k_ready + y % C::KB, y / C::KB); };
-            auto v_wait = [&](int y) { return wait(v_ready + y % C::VB, y / C::VB); };
-            while (x < NX && ok) {
-                const int n = min(w.steps - c0, NX - x);  // steps of this segment
-                if (NT == 2 && tile_rows(w, tile) == 0) {
-                    // nothing for this tile: its share of the buffers' releases, in step with the converters
+            ChunkWalk w = begin();
+            int c0 = s_start[3], x = 0;
+            bool ok = true;
+            if (warp == 1) {
+                const uint64_t qd = t5_desc(smem_u32(smem + C::OFF_Q), 128, D * 16), kd = t5_desc(smem_u32(smem + C::OFF_K), 128, D * 16);
+                int buf = 0, kphase = 0, sphase[2] = {0, 0}, qphase[2] = {0, 0};  // the next phase of each barrier
+                while (x < NX && ok) {
+                    const int n = min(w.steps - c0, NX - x);  // steps of this segment
+                    const int nt = NT == 2 && tile_rows(w, NT - 1) > 0 ? 2 : 1;
                     for (int c = 0; c < n && ok; ++c, ++x) {
-                        ok = k_wait(x) && v_wait(x);
-                        if (lane == 0) {
-                            mbar_arrive(k_free + x % C::KB);
-                            mbar_arrive(v_free + x % C::VB);
-                        }
-                    }
-                } else {
-                    for (int c = 0; c < n && ok; ++c, ++x, ++done) {
-                        if constexpr (NT == 2) {  // both products of one tile
+                        const uint64_t b = t5_plus(kd, buf * C::KHAT);
+                        ok = wait(k_ready + buf, kphase);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            if (t >= nt || !ok) break;
+                            // S is free once its last step has been read; a segment's queries are staged after that
                             if (c == 0) {
-                                // the queries are staged once the last segment's O has been read
-                                ok = k_wait(x) && wait(q_ready + tile, segs++);
-                                if (ok) qk(x);
+                                ok = wait(q_ready + t, qphase[t]);
+                                qphase[t] ^= 1;
+                                // (the last step's s_free came before these queries: its phase is skipped)
+                            } else {
+                                ok = wait(s_free + t, sphase[t] ^ 1);
                             }
-                            if (c + 1 < n && ok) {
-                                ok = k_wait(x + 1) && wait(s_free + tile, done);
-                                if (ok) qk(x + 1);
+                            sphase[t] ^= 1;
+                            if (!ok) break;
+                            if (t5_elect()) {
+                                if (t == 0) {
+#pragma unroll
+                                    for (int k = 0; k < D / 16; ++k) t5_mma_ts(tm + C::T_S, tm + C::T_Q + 8 * k, b + 16 * k, ID_S, k > 0);
+                                } else {
+#pragma unroll
+                                    for (int k = 0; k < D / 16; ++k) t5_mma_ss(tm + C::T_S + NK, qd + 16 * k, b + 16 * k, ID_S, k > 0);
+                                }
+                                t5_commit(s_ready + t);
                             }
-                            ok = ok && v_wait(x) && wait(p_ready + tile, done);
-                            if (ok) pv(x, c == 0);
-                        } else if (warp == 1) {
-                            ok = k_wait(x) && (c == 0 ? wait(q_ready, segs++) : wait(s_free, done - 1));
-                            if (ok) qk(x);
-                        } else {
-                            ok = v_wait(x) && wait(p_ready, done);
-                            if (ok) pv(x, c == 0);
+                            __syncwarp();
                         }
+                        if (ok && t5_elect()) t5_commit(k_free + buf);
+                        __syncwarp();
+                        if (++buf == C::KB) buf = 0, kphase ^= 1;
                     }
+                    if (x < NX && ok) advance(w);
+                    c0 = 0;
                 }
-                if (x < NX && ok) advance(w);
-                c0 = 0;
+            } else if (NT == 2 || warp == 2) {
+                const int tile = NT == 2 ? warp - 2 : 0;
+                const uint64_t vd = t5_desc(smem_u32(smem + C::OFF_V), 128, NK * 16);
+                const uint32_t o = t5_uniform(tm + C::T_O + tile * D), a = t5_uniform(tm + C::T_P + tile * (NK / 2));
+                int buf = 0, vphase = 0, pphase = 0;
+                while (x < NX && ok) {
+                    const int n = min(w.steps - c0, NX - x);
+                    const bool live = tile_rows(w, tile) > 0;
+                    for (int c = 0; c < n && ok; ++c, ++x) {
+                        const uint64_t b = t5_plus(vd, buf * C::VHAT);
+                        const uint32_t add = t5_uniform(c == 0 ? 0u : 1u);
+                        ok = wait(v_ready + buf, vphase);
+                        if (!live) {  // nothing for this tile: its share of the buffer's release
+                            if (lane == 0) mbar_arrive(v_free + buf);
+                        } else {
+                            ok = ok && wait(p_ready + tile, pphase);
+                            pphase ^= 1;
+                            if (ok && t5_elect()) {
+#pragma unroll
+                                for (int k = 0; k < NK / 16; ++k) t5_mma_ts(o, a + 8 * k, b + 16 * k, ID_O, k > 0 ? 1u : add);
+                                t5_commit(pv_done + tile);
+                                t5_commit(v_free + buf);
+                            }
+                            __syncwarp();
+                        }
+                        if (++buf == C::VB) buf = 0, vphase ^= 1;
+                    }
+                    if (x < NX && ok) advance(w);
+                    c0 = 0;
+                }
             }
             if (!ok && lane == 0) atomicOr(v.err, KVQ_DEVERR_TIMEOUT);
             // every MMA has completed before tensor memory is freed
@@ -894,39 +909,60 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS, LIFT>::THREADS, 1)
                 const int i = rv ? static_cast<int>(rr / G) : 0;
                 const size_t orow = (static_cast<size_t>(w.s.first) + i) * p.Hq + static_cast<size_t>(w.h) * G + (rv ? rr % G : 0);
                 const int lim = w.s.len - w.s.n + i;  // last position of the row
-                // ---- the row's query, scaled to a largest value of 2^10 .. 2^11 ----
+                // ---- the row's query as f16 ----
                 const X *src = static_cast<const X *>(p.q) + (static_cast<size_t>(w.s.first) + i) * p.q_stride +
                                (static_cast<size_t>(w.h) * G + (rv ? rr % G : 0)) * D;
                 float rs = 0.f;
                 if (live) {
-                    float top = 0.f;
-                    if (rv)
-                        for (int d = 0; d < D; d += 4) {
-                            const float4 q4 = Act<DT>::load4(src + d);
-                            top = fmaxf(top, fmaxf(fmaxf(fabsf(q4.x), fabsf(q4.y)), fmaxf(fabsf(q4.z), fabsf(q4.w))));
-                        }
-                    const int ex = static_cast<int>(__float_as_uint(top) >> 23);
-                    int k = top == 0.f || ex == 255 ? 0 : 10 - (ex - 127);
-                    k = max(-120, min(120, k));
-                    float up = __int_as_float((127 + k) << 23);
-                    rs = fabsf(p.scale) * kChunkLog2e * __int_as_float((127 - k) << 23);
-                    if (p.scale < 0.f) up = -up;  // rs >= 0: the largest score is the largest product
+                    // a part of the row is loaded at once: a load at a time would wait for memory each time
+                    constexpr int PART = LIFT ? 128 : 64;
+                    auto stage = [&](float up) {  // the row times `up` (a power of two); its largest |value|
+                        float top = 0.f;
 #pragma unroll 1
-                    for (int d0 = 0; d0 < D; d0 += 32) {
-                        uint32_t h[16];
+                        for (int p0 = 0; p0 < D; p0 += PART) {
+                            uint4 raw[PART / 8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float4 q4 = rv ? Act<DT>::load4(src + d0 + 4 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
-                            h[2 * e] = h2_as_u32(__floats2half2_rn(q4.x * up, q4.z * up));
-                            h[2 * e + 1] = h2_as_u32(__floats2half2_rn(q4.y * up, q4.w * up));
+                            for (int e = 0; e < PART / 8; ++e)
+                                raw[e] = rv ? *reinterpret_cast<const uint4 *>(src + p0 + 8 * e) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                            for (int d0 = 0; d0 < PART; d0 += 32) {
+                                uint32_t h[16];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const uint4 r4 = raw[d0 / 8 + e / 2];
+                                    const float4 q4 = Act<DT>::widen((e & 1) ? make_uint2(r4.z, r4.w) : make_uint2(r4.x, r4.y));
+                                    top = max3(top, fabsf(q4.x), fabsf(q4.y));
+                                    top = max3(top, fabsf(q4.z), fabsf(q4.w));
+                                    h[2 * e] = h2_as_u32(__floats2half2_rn(q4.x * up, q4.z * up));
+                                    h[2 * e + 1] = h2_as_u32(__floats2half2_rn(q4.y * up, q4.w * up));
+                                }
+                                if (tile == 0) {
+                                    t5_st16(trow + C::T_Q + (p0 + d0) / 2, h);
+                                } else {
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        *reinterpret_cast<uint4 *>(smem + C::OFF_Q + core_at(r, p0 + d0 + 8 * e, D)) =
+                                            make_uint4(h[4 * e], h[4 * e + 1], h[4 * e + 2], h[4 * e + 3]);
+                                }
+                            }
                         }
-                        if (tile == 0) {
-                            t5_st16(trow + C::T_Q + d0 / 2, h);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                *reinterpret_cast<uint4 *>(smem + C::OFF_Q + core_at(r, d0 + 8 * e, D)) =
-                                    make_uint4(h[4 * e], h[4 * e + 1], h[4 * e + 2], h[4 * e + 3]);
+                        return top;
+                    };
+                    // a negative scale goes to the query: rs >= 0, so the largest score is the largest product
+                    const float sign = p.scale < 0.f ? -1.f : 1.f;
+                    rs = fabsf(p.scale) * kChunkLog2e;
+                    const float top = stage(sign);
+                    if constexpr (DT == KVQ_DT_BF16) {
+                        // rows whose largest value is outside 2^-6 .. 2^15 once more, moved to 2^10 .. 2^11: f16 then
+                        // holds every value of 2^-34 of it and up to its last bit but one
+                        const int ex = static_cast<int>(__float_as_uint(top) >> 23);
+                        const bool off = top != 0.f && ex != 255 && (ex < 127 - 6 || ex > 127 + 14);
+                        if (__any_sync(0xffffffffu, off)) {
+                            keep_branch();
+                            const int k = off ? max(-120, min(120, 10 - (ex - 127))) : 0;
+                            if (tile == 0) t5_wait_st();
+                            (void)stage(sign * __int_as_float((127 + k) << 23));
+                            rs *= __int_as_float((127 - k) << 23);
                         }
                     }
                     if (tile == 0)
@@ -1067,18 +1103,6 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS, LIFT>::THREADS, 1)
                 c0 = 0;
             }
             if (!ok && lane == 0) atomicOr(v.err, KVQ_DEVERR_TIMEOUT);
-        } else if (warp == 3) {
-            if (lane == 0) {  // for the merge: the unit that this CTA starts in
-                const ChunkWalk w = begin();
-                int32_t *e = work.first + 8 * blockIdx.x;
-                e[0] = w.b;
-                e[1] = w.h;
-                e[2] = w.u;
-                e[3] = x0 - s_start[3];  // its first step
-                e[4] = w.steps;
-                e[5] = span;
-            }
-            __syncwarp();
         }
     } else if (threadIdx.x == 0) {
         work.first[8 * blockIdx.x + 4] = 0;  // nothing starts here
