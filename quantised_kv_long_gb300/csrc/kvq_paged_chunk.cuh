@@ -523,11 +523,11 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS, LIFT>::THREADS, 1)
         }
         for (int i = 0; i < C::KB; ++i) {
             mbar_init(k_ready + i, LIFT ? 1 : C::HALF);
-            mbar_init(k_free + i, 1);
+            mbar_init(k_free + i, NT);
         }
         for (int i = 0; i < C::VB; ++i) {
             mbar_init(v_ready + i, LIFT ? 1 : C::HALF);
-            mbar_init(v_free + i, NT);
+            mbar_init(v_free + i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_ready + i, 1);
@@ -772,72 +772,68 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS, LIFT>::THREADS, 1)
             ChunkWalk w = begin();
             int c0 = s_start[3], x = 0;
             bool ok = true;
-            if (warp == 1) {
+            if (warp == 1 || (NT == 2 && warp == 2)) {
+                const int tile = warp - 1;
                 const uint64_t qd = t5_desc(smem_u32(smem + C::OFF_Q), 128, D * 16), kd = t5_desc(smem_u32(smem + C::OFF_K), 128, D * 16);
-                int buf = 0, kphase = 0, sphase[2] = {0, 0}, qphase[2] = {0, 0};  // the next phase of each barrier
+                int buf = 0, kphase = 0, sphase = 0, qphase = 0;  // the next phase of each barrier
                 while (x < NX && ok) {
                     const int n = min(w.steps - c0, NX - x);  // steps of this segment
-                    const int nt = NT == 2 && tile_rows(w, NT - 1) > 0 ? 2 : 1;
+                    const bool live = tile_rows(w, tile) > 0;
                     for (int c = 0; c < n && ok; ++c, ++x) {
                         const uint64_t b = t5_plus(kd, buf * C::KHAT);
                         ok = wait(k_ready + buf, kphase);
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            if (t >= nt || !ok) break;
-                            // S is free once its last step has been read; a segment's queries are staged after that
+                        if (!live) {
+                            if (lane == 0) mbar_arrive(k_free + buf);
+                        } else {
                             if (c == 0) {
-                                ok = wait(q_ready + t, qphase[t]);
-                                qphase[t] ^= 1;
-                                // (the last step's s_free came before these queries: its phase is skipped)
+                                ok = ok && wait(q_ready + tile, qphase);
+                                qphase ^= 1;
                             } else {
-                                ok = wait(s_free + t, sphase[t] ^ 1);
+                                ok = ok && wait(s_free + tile, sphase ^ 1);
                             }
-                            sphase[t] ^= 1;
-                            if (!ok) break;
-                            if (t5_elect()) {
-                                if (t == 0) {
+                            sphase ^= 1;
+                            if (ok && t5_elect()) {
+                                if (tile == 0) {
 #pragma unroll
                                     for (int k = 0; k < D / 16; ++k) t5_mma_ts(tm + C::T_S, tm + C::T_Q + 8 * k, b + 16 * k, ID_S, k > 0);
                                 } else {
 #pragma unroll
                                     for (int k = 0; k < D / 16; ++k) t5_mma_ss(tm + C::T_S + NK, qd + 16 * k, b + 16 * k, ID_S, k > 0);
                                 }
-                                t5_commit(s_ready + t);
+                                t5_commit(s_ready + tile);
+                                t5_commit(k_free + buf);
                             }
                             __syncwarp();
                         }
-                        if (ok && t5_elect()) t5_commit(k_free + buf);
-                        __syncwarp();
                         if (++buf == C::KB) buf = 0, kphase ^= 1;
                     }
                     if (x < NX && ok) advance(w);
                     c0 = 0;
                 }
             } else if (NT == 2 || warp == 2) {
-                const int tile = NT == 2 ? warp - 2 : 0;
                 const uint64_t vd = t5_desc(smem_u32(smem + C::OFF_V), 128, NK * 16);
-                const uint32_t o = t5_uniform(tm + C::T_O + tile * D), a = t5_uniform(tm + C::T_P + tile * (NK / 2));
-                int buf = 0, vphase = 0, pphase = 0;
+                int buf = 0, vphase = 0, pphase[2] = {0, 0};
                 while (x < NX && ok) {
                     const int n = min(w.steps - c0, NX - x);
-                    const bool live = tile_rows(w, tile) > 0;
+                    const int nt = NT == 2 && tile_rows(w, NT - 1) > 0 ? 2 : 1;
                     for (int c = 0; c < n && ok; ++c, ++x) {
                         const uint64_t b = t5_plus(vd, buf * C::VHAT);
                         const uint32_t add = t5_uniform(c == 0 ? 0u : 1u);
                         ok = wait(v_ready + buf, vphase);
-                        if (!live) {  // nothing for this tile: its share of the buffer's release
-                            if (lane == 0) mbar_arrive(v_free + buf);
-                        } else {
-                            ok = ok && wait(p_ready + tile, pphase);
-                            pphase ^= 1;
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            if (t >= nt || !ok) break;
+                            ok = wait(p_ready + t, pphase[t]);
+                            pphase[t] ^= 1;
                             if (ok && t5_elect()) {
 #pragma unroll
-                                for (int k = 0; k < NK / 16; ++k) t5_mma_ts(o, a + 8 * k, b + 16 * k, ID_O, k > 0 ? 1u : add);
-                                t5_commit(pv_done + tile);
-                                t5_commit(v_free + buf);
+                                for (int k = 0; k < NK / 16; ++k) t5_mma_ts(tm + C::T_O + t * D, tm + C::T_P + t * (NK / 2) + 8 * k, b + 16 * k, ID_O, k > 0 ? 1u : add);
+                                t5_commit(pv_done + t);
                             }
                             __syncwarp();
                         }
+                        if (ok && t5_elect()) t5_commit(v_free + buf);
+                        __syncwarp();
                         if (++buf == C::VB) buf = 0, vphase ^= 1;
                     }
                     if (x < NX && ok) advance(w);
