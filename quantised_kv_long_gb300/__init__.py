@@ -512,8 +512,9 @@ class PagedCache:
             if max_q is None:
                 max_q = max(1, n_tokens)
         width = shape[1]
+        # one row has any stride; rows that overlap (an expanded table) are refused by the call itself
         return PagedBatch(n_seqs, n_tokens, max_q, width * self.page_size if max_len is None else max_len, cu, lens.data_ptr(),
-                          block_table.data_ptr(), width, max(width, strides[0]))
+                          block_table.data_ptr(), width, strides[0] if n_seqs > 1 else max(width, strides[0]))
 
     def _rows(self, t, heads, what, dtype=None):
         """Packed rows [n_tokens, heads, D] with contiguous heads and values: (pointer, token stride)."""

@@ -228,13 +228,13 @@ struct PagedAttnParams {
 cudaError_t launch_paged_append(int type_k, int type_v, int D, int dtype, const PagedAppendParams &p, cudaStream_t s);
 cudaError_t launch_paged_gather(int type_k, int type_v, int D, int dtype, const PagedGatherParams &p, cudaStream_t s);
 cudaError_t launch_paged_attention(int type_k, int type_v, int D, int dtype, const PagedAttnParams &p, cudaStream_t s);
-// workspace bytes of a call; sizes known on the host only
+// workspace bytes of a call, from sizes known on the host; cudaErrorNotSupported past kPagedMaxSteps
 cudaError_t paged_attention_workspace(int type_k, int type_v, int D, int dtype, const PagedAttnParams &p, size_t *bytes);
 // few queries per sequence (kvq_paged_split.cuh), one translation unit per activation type
 cudaError_t launch_paged_split_f32(int type_k, int type_v, int D, const PagedAttnParams &p, cudaStream_t s);
 cudaError_t launch_paged_split_f16(int type_k, int type_v, int D, const PagedAttnParams &p, cudaStream_t s);
 cudaError_t launch_paged_split_bf16(int type_k, int type_v, int D, const PagedAttnParams &p, cudaStream_t s);
-cudaError_t paged_split_workspace(int D, size_t *bytes);
+cudaError_t paged_split_workspace(int D, const PagedAttnParams &p, size_t *bytes);
 // many queries per sequence (kvq_paged_chunk.cuh)
 cudaError_t launch_paged_chunk_f16(int type_k, int type_v, int D, const PagedAttnParams &p, cudaStream_t s);
 cudaError_t launch_paged_chunk_bf16(int type_k, int type_v, int D, const PagedAttnParams &p, cudaStream_t s);
@@ -256,6 +256,14 @@ inline cudaError_t paged_device(int *dev, int *sms) {
     }
     *sms = cached[*dev];
     return cudaSuccess;
+}
+// Steps of one sequence, over all KV heads, that the attention kernels can count: their sums over a launch are
+// 32-bit.  A call whose sizes allow more is refused.
+constexpr long long kPagedMaxSteps = 1ll << 30;
+// most steps of a sequence: `blocks` of keys times units of `unit` rows; at least 1, at most kPagedMaxSteps + 1
+inline long long paged_steps(long long blocks, long long rows, int unit, int Hkv) {
+    const __int128 n = static_cast<__int128>(blocks) * ((rows + unit - 1) / unit) * Hkv;
+    return n > kPagedMaxSteps ? kPagedMaxSteps + 1 : (n > 1 ? static_cast<long long>(n) : 1);
 }
 // sequences b .. b + most - 1 of a call
 inline PagedAttnParams paged_some(const PagedAttnParams &p, int b, int most) {

@@ -44,6 +44,7 @@ kvq_status check_batch(const kvq_paged *c, const kvq_paged_batch *b, kvq::PagedV
     if (b->n_seqs == 0 || b->n_tokens == 0) return KVQ_OK;
     if (b->max_q < 1 || b->max_len < 0 || b->table_width < 1 || b->table_stride < b->table_width) return KVQ_ERR_INVALID_ARG;
     if (b->max_len > static_cast<long long>(b->table_width) * c->desc.page_size) return KVQ_ERR_INVALID_ARG;
+    if (b->max_len > INT32_MAX - 1024) return KVQ_ERR_UNSUPPORTED;  // the kernels round lengths up to blocks in 32 bits
     if (!b->lens || !b->block_table) return KVQ_ERR_INVALID_ARG;
     if (!b->cu_q && b->n_tokens < b->n_seqs) return KVQ_ERR_INVALID_ARG;
     if (!aligned4(b->lens) || !aligned4(b->block_table) || !aligned4(b->cu_q)) return KVQ_ERR_ALIGNMENT;
@@ -94,6 +95,11 @@ kvq_status attention_params(const kvq_paged *c, const kvq_paged_batch *b, int32_
     p->Hq = n_q_heads;
     p->G = n_q_heads / c->desc.n_kv_heads;
     return KVQ_OK;
+}
+
+kvq_status workspace_of(const kvq_paged *c, kvq_dtype dtype, const kvq::PagedAttnParams &p, size_t *bytes) {
+    const cudaError_t e = kvq::paged_attention_workspace(c->desc.type_k, c->desc.type_v, c->desc.head_dim, dtype, p, bytes);
+    return e == cudaSuccess ? KVQ_OK : e == cudaErrorNotSupported ? KVQ_ERR_UNSUPPORTED : KVQ_ERR_CUDA;
 }
 
 }  // namespace
@@ -211,10 +217,7 @@ kvq_status kvq_paged_attention_workspace_size(const kvq_paged *cache, const kvq_
     *bytes = 16;
     if (batch->n_seqs == 0 || batch->n_tokens == 0) return KVQ_OK;
     KVQ_TRY(check_device(cache));
-    return kvq::paged_attention_workspace(cache->desc.type_k, cache->desc.type_v, cache->desc.head_dim, dtype, p, bytes) ==
-                   cudaSuccess
-               ? KVQ_OK
-               : KVQ_ERR_CUDA;
+    return workspace_of(cache, dtype, p, bytes);
 }
 
 kvq_status kvq_paged_attention(const kvq_paged *cache, const kvq_paged_batch *batch, const void *q, kvq_dtype dtype,
@@ -229,7 +232,7 @@ kvq_status kvq_paged_attention(const kvq_paged *cache, const kvq_paged_batch *ba
     KVQ_TRY(check_device(cache));
     const int tk = cache->desc.type_k, tv = cache->desc.type_v, D = cache->desc.head_dim;
     size_t need = 0;
-    if (kvq::paged_attention_workspace(tk, tv, D, dtype, p, &need) != cudaSuccess) return KVQ_ERR_CUDA;
+    KVQ_TRY(workspace_of(cache, dtype, p, &need));
     if (workspace_bytes < need) return KVQ_ERR_SCRATCH;
     p.q = q;
     p.out = out;

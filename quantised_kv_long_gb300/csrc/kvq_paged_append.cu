@@ -197,9 +197,11 @@ __device__ __forceinline__ Piece find_piece(const PagedView &v, int p) {
     c.b = lo;
     c.s = paged_seq(v, lo);
     const int k = p - ((c.s.first >> 4) + 2 * lo), pos0 = c.s.len - c.s.n;  // pos0 < 0: tokens before position 0
-    c.tile = (max(pos0, 0) >> 4) + k;
+    const int tile0 = max(pos0, 0) >> 4, tiles = (c.s.len + (kTileRows - 1)) / kTileRows;
+    const bool any = k >= 0 && k < tiles - tile0 && c.s.n > 0;  // else no tile of the sequence
+    c.tile = any ? tile0 + k : tile0;
     c.r0 = max(0, max(pos0, 0) - c.tile * kTileRows);
-    c.r1 = k >= 0 && c.s.n > 0 ? min(kTileRows, c.s.len - c.tile * kTileRows) : 0;
+    c.r1 = any ? min(kTileRows, c.s.len - c.tile * kTileRows) : 0;
     return c;
 }
 __host__ __device__ inline long long piece_bound(const PagedView &v) { return v.n_tokens / kTileRows + 2ll * v.n_seqs; }

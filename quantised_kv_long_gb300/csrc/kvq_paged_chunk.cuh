@@ -370,13 +370,18 @@ struct ChunkWork {
 };
 constexpr size_t kLiftBytes = size_t(2) << 30;  // most that lifted operands may take
 
+// Most steps that one sequence of the call can have.
+inline long long chunk_seq_steps(const PagedAttnParams &p, int rows) {
+    return paged_steps((static_cast<long long>(p.v.max_len) + kChunkKeys) / kChunkKeys, static_cast<long long>(p.v.max_q) * p.G, rows, p.v.Hkv);
+}
+
 // Blocks (of one KV head) that the chunk class of a call can have, all heads together; 0 if their operands
 // would pass kLiftBytes.
 inline long long lift_blocks(const PagedAttnParams &p, int D) {
     const long long seqs = p.v.n_tokens / p.from_q < p.v.n_seqs ? p.v.n_tokens / p.from_q : p.v.n_seqs;
     const long long per = p.v.max_len > 0 ? (static_cast<long long>(p.v.max_len) + kChunkKeys - 1) / kChunkKeys : 1;
-    const long long n = seqs * per * p.v.Hkv;
-    return n <= static_cast<long long>(kLiftBytes / (kChunkKeys * D * 4)) ? n : 0;
+    const long long most = static_cast<long long>(kLiftBytes / (kChunkKeys * D * 4)), one = per * p.v.Hkv;
+    return one <= most && seqs * one <= most ? seqs * one : 0;
 }
 inline ChunkWork chunk_work(const PagedAttnParams &p, int ctas, int rows, int D, size_t *bytes) {
     uint8_t *w = static_cast<uint8_t *>(p.workspace);
@@ -950,7 +955,8 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS, LIFT>::THREADS, 1)
                     const float top = stage(sign);
                     if constexpr (DT == KVQ_DT_BF16) {
                         // rows whose largest value is outside 2^-6 .. 2^15 once more, moved to 2^10 .. 2^11: f16 then
-                        // holds every value of 2^-34 of it and up to its last bit but one
+                        // holds values down to 2^-27 of it exactly, smaller ones to 2^-35 of it (inside, the least
+                        // case is a largest value of 2^-6: to 2^-19 of it)
                         const int ex = static_cast<int>(__float_as_uint(top) >> 23);
                         const bool off = top != 0.f && ex != 255 && (ex < 127 - 6 || ex > 127 + 14);
                         if (__any_sync(0xffffffffu, off)) {
@@ -1187,11 +1193,9 @@ cudaError_t launch_chunk_t(const PagedAttnParams &p, cudaStream_t stream) {
     }
     const ChunkWork work = chunk_work(p, sms, C::ROWS, C::D, nullptr);
     // sequences of one launch: their prefix sums fit shared memory, their steps 2^30
-    const long long units = (static_cast<long long>(p.v.max_q) * p.G + C::ROWS - 1) / C::ROWS;
-    const long long per_seq = units * ((p.v.max_len + C::NK) / C::NK) * p.v.Hkv;
-    const long long fit = (1ll << 30) / per_seq;
+    const long long fit = kPagedMaxSteps / chunk_seq_steps(p, C::ROWS);
     const int most = static_cast<int>(fit < kChunkMaxSeqs ? fit : kChunkMaxSeqs);
-    if (most < 1) return cudaErrorInvalidValue;
+    if (most < 1) return cudaErrorNotSupported;
     for (int b = 0; b < p.v.n_seqs; b += most) {
         const PagedAttnParams q = paged_some(p, b, most);
         if (LIFT) {

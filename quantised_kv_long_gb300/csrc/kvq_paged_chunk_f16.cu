@@ -11,7 +11,9 @@ cudaError_t paged_chunk_workspace(int D, const PagedAttnParams &p, size_t *bytes
     int dev = 0, sms = 0;
     const cudaError_t e = paged_device(&dev, &sms);
     if (e != cudaSuccess) return e;
-    (void)chunk_work(p, sms, D == kSlice ? ChunkCfg<KVQ_F16, KVQ_F16, 1, true>::ROWS : ChunkCfg<KVQ_F16, KVQ_F16, 2, true>::ROWS, D, bytes);
+    const int rows = D == kSlice ? ChunkCfg<KVQ_F16, KVQ_F16, 1, true>::ROWS : ChunkCfg<KVQ_F16, KVQ_F16, 2, true>::ROWS;
+    if (chunk_seq_steps(p, rows) > kPagedMaxSteps) return cudaErrorNotSupported;
+    (void)chunk_work(p, sms, rows, D, bytes);
     return cudaSuccess;
 }
 

@@ -982,6 +982,13 @@ __global__ void __launch_bounds__(NS * 32 * kMergeWays)
 }
 
 constexpr int kSplitMaxWarps = 16;
+// Most query rows per KV head, and most steps, of a sequence of this kernel's class.
+inline long long split_max_rows(const PagedAttnParams &p) {
+    return static_cast<long long>(p.v.max_q < p.from_q ? p.v.max_q : p.from_q - 1) * p.G;
+}
+inline long long split_seq_steps(const PagedAttnParams &p) {
+    return paged_steps((static_cast<long long>(p.v.max_len) + kTileRows - 1) / kTileRows, split_max_rows(p), kRows, p.v.Hkv);
+}
 // One CTA per unit, or equal spans?  A unit costs its CTA about 4.5 us + 4.9 us per 1024 keys; equal spans
 // cost 9.5 us (sums over the batch, the merge) and then 2 us + 4.7 us per 1024 keys for each unit per SM
 // (q4_0, 128-wide; measured over 1 to 128 sequences of 8 KV heads, 128 to 4096 positions: 8 units of 128 /
@@ -1013,13 +1020,11 @@ cudaError_t launch_split_t(const PagedAttnParams &p, cudaStream_t stream) {
         configured[dev] = true;
     }
     const SplitWork work = split_work(p.workspace, 2 * kSplitMaxWarps * sms);
-    const int max_q = p.v.max_q < p.from_q ? p.v.max_q : p.from_q - 1;
-    const int max_groups = static_cast<int>((static_cast<long long>(max_q) * p.G + kRows - 1) / kRows);
+    const int max_groups = static_cast<int>((split_max_rows(p) + kRows - 1) / kRows);
     // sequences of one launch: their prefix sums fit shared memory, their steps 2^30
-    const long long per_seq = static_cast<long long>(p.v.max_len + kTileRows - 1) / kTileRows * p.v.Hkv * max_groups;
-    const long long fit = per_seq > 0 ? (1ll << 30) / per_seq : kSplitMaxSeqs;
+    const long long fit = kPagedMaxSteps / split_seq_steps(p);
     const int most = static_cast<int>(fit < kSplitMaxSeqs ? fit : kSplitMaxSeqs);
-    if (most < 1) return cudaErrorInvalidValue;
+    if (most < 1) return cudaErrorNotSupported;
     for (int b = 0; b < p.v.n_seqs; b += most) {
         const PagedAttnParams q = paged_some(p, b, most);
         const long long units = static_cast<long long>(q.v.n_seqs) * p.v.Hkv * max_groups;

@@ -175,3 +175,12 @@ def test_binding_refuses_what_it_cannot_pass():
     assert c._rows(fused[:, 2:4], 2, "k") == (fused.data_ptr() + 2 * 128 * 2, 6 * 128)
     with pytest.raises(ValueError):
         kvq.Rope(torch.zeros((4, 8)))
+
+
+def test_lengths_near_32_bits_are_refused():
+    """Lengths are rounded up to whole blocks in 32 bits on the device."""
+    h, L, sz = fake_handle(), kvq.lib, ctypes.c_size_t()
+    for max_len, status in ((2**31 - 1, 2), (2**31 - 1024, 2)):
+        b = batch(max_len=max_len, table_width=2**28, table_stride=2**28)
+        assert L.kvq_paged_gather(ctypes.byref(h), ctypes.byref(b), FAKE, FAKE, 0, None) == status
+        assert L.kvq_paged_attention_workspace_size(ctypes.byref(h), ctypes.byref(b), 4, 0, ctypes.byref(sz)) == status
