@@ -238,7 +238,7 @@ cudaError_t paged_split_workspace(int D, const PagedAttnParams &p, size_t *bytes
 // many queries per sequence (kvq_paged_chunk.cuh)
 cudaError_t launch_paged_chunk_f16(int type_k, int type_v, int D, const PagedAttnParams &p, cudaStream_t s);
 cudaError_t launch_paged_chunk_bf16(int type_k, int type_v, int D, const PagedAttnParams &p, cudaStream_t s);
-cudaError_t paged_chunk_workspace(int D, const PagedAttnParams &p, size_t *bytes);
+cudaError_t paged_chunk_workspace(int type_k, int D, int dtype, const PagedAttnParams &p, size_t *bytes);
 
 // ---- what the attention launches share ----
 constexpr int kPagedMaxDevices = 64;

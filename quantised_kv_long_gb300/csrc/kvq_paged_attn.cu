@@ -39,7 +39,7 @@ cudaError_t paged_attention_workspace(int type_k, int, int D, int dtype, const P
     // the two kernels of a mixed call run one after the other and share it
     size_t split = 0, chunk = 0;
     cudaError_t e = p.from_q > 1 ? paged_split_workspace(D, p, &split) : cudaSuccess;
-    if (e == cudaSuccess && p.v.max_q >= p.from_q) e = paged_chunk_workspace(D, p, &chunk);
+    if (e == cudaSuccess && p.v.max_q >= p.from_q) e = paged_chunk_workspace(type_k, D, dtype, p, &chunk);
     *bytes = split > chunk ? split : chunk;
     return e;
 }

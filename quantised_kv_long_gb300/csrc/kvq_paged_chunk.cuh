@@ -27,8 +27,9 @@
 // sixteen, so that a warp's stores of V^ fill whole core matrices; the epilogue puts them back.
 //
 // Rounding.  Q is f16; a bf16 row outside f16's range is moved by a power of two.
-// K^ and V^ are scale x code rounded once to f16 (2^-11), P is f16 (2^-11); S, O, the maxima and
-// sums are fp32.  The output has 16 bits (2^-11 or 2^-8).  A block with scales that would leave f16
+// K^ and V^ are scale x code rounded once to f16 (2^-11), P is f16 (2^-11); with f16 activations over
+// quantised pages K^ and P are pairs hi + lo (chunk_fine).  S, O, the maxima and sums are
+// fp32.  The output has 16 bits (2^-11 or 2^-8).  A block with scales that would leave f16
 // is stored times 2^-e, and S or P is multiplied by 2^e, both exact.
 #pragma once
 #include <math_constants.h>
@@ -216,7 +217,8 @@ __device__ __forceinline__ int block_exp(TileAt tile, const BlockRows &use) {
 
 // K^ of a block times 2^-e, by warps cw, cw + nw, ..: rows past the sequence's end may become anything (their
 // scores are masked).  tile(i): record of tile i; kh: the operand, shared or global memory.
-template <int KT, int VT, int NS, class TileAt>
+// FINE: hi = f16(scale x code) and, an operand further on, lo = scale x code - hi.
+template <int KT, int VT, int NS, bool FINE, class TileAt>
 __device__ __forceinline__ void convert_keys(TileAt tile, uint8_t *kh, int e, int cw, const int nw) {
     using T = PagedTile<KT, VT, NS>;
     constexpr int D = T::D;
@@ -224,7 +226,11 @@ __device__ __forceinline__ void convert_keys(TileAt tile, uint8_t *kh, int e, in
     const __half2 fk = __float2half2_rn(pow2i_f(KT == KVQ_Q8_0 ? 10 - e : -e));
     uint8_t *lane_at = kh + (jd >> 1) * 128 + n * 16 + (jd & 1) * 8;  // core_at(n, 4 jd, D)
     auto put = [&](int at, __half2 c02, __half2 c13, __half2 d2) {
-        *reinterpret_cast<uint2 *>(lane_at + at) = make_uint2(h2_as_u32(__hmul2(c02, d2)), h2_as_u32(__hmul2(c13, d2)));
+        const __half2 a = __hmul2(c02, d2), b = __hmul2(c13, d2);
+        *reinterpret_cast<uint2 *>(lane_at + at) = make_uint2(h2_as_u32(a), h2_as_u32(b));
+        if constexpr (FINE)
+            *reinterpret_cast<uint2 *>(lane_at + at + kChunkKeys * D * 2) =
+                make_uint2(h2_as_u32(__hfma2(c02, d2, __hneg2(a))), h2_as_u32(__hfma2(c13, d2, __hneg2(b))));
     };
     // core_at(16 i + n + 8 s8, dim + 4 jd, D) less lane_at, for dim a multiple of 16
     auto at = [](int i, int s8, int dim) { return (2 * i + s8) * (D * 16) + dim * 16; };
@@ -331,18 +337,27 @@ __device__ __forceinline__ void convert_values(TileAt tile, uint8_t *vh, int e, 
     }
 }
 
-template <int KT, int VT, int NS, bool LIFT>
+// FINE (f16 activations over quantised pages): K^ is a pair hi + lo and so are the weights, twice the products.
+// One f16 rounding each of K^, V^ and P adds 3.6e-4 to 8.4e-4 of the outputs' norm (the more the wider the scores) to
+// the 2.1e-4 of an f16 output's own rounding (bf16: 1.7e-3); with the pairs V^'s alone is left, 2.1e-4.
+template <int KT, int DT>
+constexpr bool chunk_fine() { return KT != KVQ_F16 && DT == KVQ_DT_F16; }
+
+template <int KT, int VT, int NS, bool LIFT, bool FINE>
 struct ChunkCfg {
     using T = PagedTile<KT, VT, NS>;
     static constexpr int D = T::D, M = 128, NK = kChunkKeys, TILES = kChunkTiles;
     static constexpr int NT = NS == 1 ? 2 : 1;  // tiles of 128 rows per unit
     static constexpr int ROWS = NT * M;
-    static constexpr int KHAT = NK * D * 2, VHAT = NK * D * 2, IMAGE = KHAT + VHAT;
-    static constexpr int QSM = NT == 2 ? M * D * 2 : 0;  // Q of tile 1 (tile 0's is in tensor memory)
+    static constexpr int PARTS = FINE ? 2 : 1;  // of K^ and of P
+    static constexpr int KHAT = PARTS * NK * D * 2, VHAT = NK * D * 2, IMAGE = KHAT + VHAT;
+    // Q of tile 0 is in tensor memory where there is room, of the others in shared memory
+    static constexpr bool Q0_TMEM = !(FINE && NT == 2);
+    static constexpr int QSM = (NT - (Q0_TMEM ? 1 : 0)) * M * D * 2;
     static constexpr int LIMIT = 232448 - 3072;          // of the CTA's shared memory, barriers and statics kept back
-    // operand buffers: all that fit when lifted, else two of each, or one of V^ where two raw stages would not fit
+    // operand buffers: all that fit when lifted, else two of each, or one where two raw stages would not fit
     static constexpr int STAGE = LIFT ? 1 : TILES * T::BYTES;
-    static constexpr int KB = LIFT ? (LIMIT - QSM) / IMAGE : 2;
+    static constexpr int KB = LIFT ? (LIMIT - QSM) / IMAGE : (FINE && NS == 2 ? 1 : 2);
     static constexpr int VB = LIFT ? KB : ((LIMIT - QSM - KB * KHAT - 2 * VHAT) / STAGE >= 2 ? 2 : 1);
     static constexpr int OPS = QSM + KB * KHAT + VB * VHAT;
     static constexpr int STAGES_RAW = (LIMIT - OPS) / STAGE;
@@ -350,12 +365,14 @@ struct ChunkCfg {
     static constexpr int OFF_Q = STAGES * STAGE, OFF_K = OFF_Q + QSM, OFF_V = OFF_K + KB * KHAT;
     static constexpr int SMEM = OFF_V + VB * VHAT;
     // tensor memory columns: O of each tile, S of each, P of each, Q of tile 0
-    static constexpr int T_O = 0, T_S = NT * D, T_P = T_S + NT * NK, T_Q = T_P + NT * NK / 2;
-    static_assert(T_Q + D / 2 <= 512, "tensor memory");
-    static_assert((LIFT || STAGES >= 2) && KB >= 2 && KB <= 6 && SMEM <= LIMIT, "shared memory");
+    static constexpr int PCOLS = PARTS * NK / 2;
+    static constexpr int T_O = 0, T_S = NT * D, T_P = T_S + NT * NK, T_Q = T_P + NT * PCOLS;
+    static_assert(T_Q + (Q0_TMEM ? D / 2 : 0) <= 512, "tensor memory");
+    static_assert((LIFT || STAGES >= 2) && KB >= 1 && (!LIFT || KB >= 2) && VB >= 1 && KB <= 6 && SMEM <= LIMIT, "shared memory");
     static constexpr int SOFT0 = 4, CONV0 = SOFT0 + 4 * NT, CONV_WARPS = LIFT ? 0 : 8;  // first softmax / converter warp
     static constexpr int HALF = CONV_WARPS / 2;                                         // converters of K^, and of V^
     static constexpr int WARPS = CONV0 + CONV_WARPS;
+    static constexpr int q_at(int tile) { return OFF_Q + (Q0_TMEM && tile > 0 ? tile - 1 : tile) * M * D * 2; }  // if not in tensor memory
     static constexpr int THREADS = WARPS * 32;
 };
 
@@ -377,20 +394,21 @@ inline long long chunk_seq_steps(const PagedAttnParams &p, int rows) {
 
 // Blocks (of one KV head) that the chunk class of a call can have, all heads together; 0 if their operands
 // would pass kLiftBytes.
-inline long long lift_blocks(const PagedAttnParams &p, int D) {
+inline size_t image_bytes(int D, bool fine) { return static_cast<size_t>(kChunkKeys) * D * (fine ? 6 : 4); }
+inline long long lift_blocks(const PagedAttnParams &p, int D, bool fine) {
     const long long seqs = p.v.n_tokens / p.from_q < p.v.n_seqs ? p.v.n_tokens / p.from_q : p.v.n_seqs;
     const long long per = p.v.max_len > 0 ? (static_cast<long long>(p.v.max_len) + kChunkKeys - 1) / kChunkKeys : 1;
-    const long long most = static_cast<long long>(kLiftBytes / (kChunkKeys * D * 4)), one = per * p.v.Hkv;
+    const long long most = static_cast<long long>(kLiftBytes / image_bytes(D, fine)), one = per * p.v.Hkv;
     return one <= most && seqs * one <= most ? seqs * one : 0;
 }
-inline ChunkWork chunk_work(const PagedAttnParams &p, int ctas, int rows, int D, size_t *bytes) {
+inline ChunkWork chunk_work(const PagedAttnParams &p, int ctas, int rows, int D, bool fine, size_t *bytes) {
     uint8_t *w = static_cast<uint8_t *>(p.workspace);
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     const size_t ml = up(static_cast<size_t>(ctas) * 32), o = ml + up(static_cast<size_t>(2) * ctas * rows * 8);
     const size_t info = o + up(static_cast<size_t>(2) * ctas * rows * D * 4);
-    const long long cap = lift_blocks(p, D);
+    const long long cap = lift_blocks(p, D, fine);
     const size_t image = info + up(static_cast<size_t>(cap) * 16);
-    if (bytes) *bytes = image + static_cast<size_t>(cap) * kChunkKeys * D * 4;
+    if (bytes) *bytes = image + static_cast<size_t>(cap) * image_bytes(D, fine);
     return ChunkWork{reinterpret_cast<int32_t *>(w), reinterpret_cast<float *>(w + ml), reinterpret_cast<float *>(w + o),
                      reinterpret_cast<int4 *>(w + info), w + image, static_cast<int>(cap)};
 }
@@ -442,9 +460,9 @@ __device__ __forceinline__ void warp_prefix(int *a, int n) {
 
 // The operands of every block of the sequences of the chunk class: one warp per (block, K^ or V^).
 constexpr int kLiftWarps = 8;
-template <int KT, int VT, int NS>
+template <int KT, int VT, int NS, bool FINE>
 __global__ void __launch_bounds__(32 * kLiftWarps) paged_lift_kernel(const PagedAttnParams p, const ChunkWork work) {
-    using C = ChunkCfg<KT, VT, NS, true>;
+    using C = ChunkCfg<KT, VT, NS, true, FINE>;
     using T = typename C::T;
     __shared__ int s_blocks[kChunkMaxSeqs + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -487,7 +505,7 @@ __global__ void __launch_bounds__(32 * kLiftWarps) paged_lift_kernel(const Paged
         if (keys) {
             const int e = block_exp<KT, T::OFF_KS, NS>(tile, use);
             if (lane == 0) info[0] = use.got, info[1] = e;
-            convert_keys<KT, VT, NS>(tile, image, e, 0, 1);
+            convert_keys<KT, VT, NS, FINE>(tile, image, e, 0, 1);
         } else {
             const int e = block_exp<VT, T::OFF_VS, NS>(tile, use);
             if (lane == 0) info[2] = e;
@@ -504,9 +522,10 @@ struct ChunkWalk {
 };
 
 template <int KT, int VT, int NS, int DT, bool LIFT>
-__global__ void __launch_bounds__(ChunkCfg<KT, VT, NS, LIFT>::THREADS, 1)
+__global__ void __launch_bounds__(ChunkCfg<KT, VT, NS, LIFT, chunk_fine<KT, DT>()>::THREADS, 1)
     paged_chunk_kernel(const PagedAttnParams p, const ChunkWork work) {
-    using C = ChunkCfg<KT, VT, NS, LIFT>;
+    constexpr bool FINE = chunk_fine<KT, DT>();
+    using C = ChunkCfg<KT, VT, NS, LIFT, FINE>;
     using T = typename C::T;
     using X = typename Act<DT>::type;
     constexpr int D = C::D, NK = C::NK, NT = C::NT, ROWS = C::ROWS;
@@ -779,7 +798,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS, LIFT>::THREADS, 1)
             bool ok = true;
             if (warp == 1 || (NT == 2 && warp == 2)) {
                 const int tile = warp - 1;
-                const uint64_t qd = t5_desc(smem_u32(smem + C::OFF_Q), 128, D * 16), kd = t5_desc(smem_u32(smem + C::OFF_K), 128, D * 16);
+                const uint64_t qd = t5_desc(smem_u32(smem + C::q_at(tile)), 128, D * 16), kd = t5_desc(smem_u32(smem + C::OFF_K), 128, D * 16);
                 int buf = 0, kphase = 0, sphase = 0, qphase = 0;  // the next phase of each barrier
                 while (x < NX && ok) {
                     const int n = min(w.steps - c0, NX - x);  // steps of this segment
@@ -798,12 +817,14 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS, LIFT>::THREADS, 1)
                             }
                             sphase ^= 1;
                             if (ok && t5_elect()) {
-                                if (tile == 0) {
+                                // lo follows hi by NK D 2 bytes
+                                constexpr int QK = D / 16, LO = NK * D * 2 / 16 - 16 * QK;
+                                if (C::Q0_TMEM && tile == 0) {
 #pragma unroll
-                                    for (int k = 0; k < D / 16; ++k) t5_mma_ts(tm + C::T_S, tm + C::T_Q + 8 * k, b + 16 * k, ID_S, k > 0);
+                                    for (int k = 0; k < C::PARTS * QK; ++k) t5_mma_ts(tm + C::T_S, tm + C::T_Q + 8 * (k % QK), b + 16 * k + k / QK * LO, ID_S, k > 0);
                                 } else {
 #pragma unroll
-                                    for (int k = 0; k < D / 16; ++k) t5_mma_ss(tm + C::T_S + NK, qd + 16 * k, b + 16 * k, ID_S, k > 0);
+                                    for (int k = 0; k < C::PARTS * QK; ++k) t5_mma_ss(tm + C::T_S + tile * NK, qd + 16 * (k % QK), b + 16 * k + k / QK * LO, ID_S, k > 0);
                                 }
                                 t5_commit(s_ready + tile);
                                 t5_commit(k_free + buf);
@@ -832,7 +853,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS, LIFT>::THREADS, 1)
                             pphase[t] ^= 1;
                             if (ok && t5_elect()) {
 #pragma unroll
-                                for (int k = 0; k < NK / 16; ++k) t5_mma_ts(tm + C::T_O + t * D, tm + C::T_P + t * (NK / 2) + 8 * k, b + 16 * k, ID_O, k > 0 ? 1u : add);
+                                for (int k = 0; k < C::PARTS * NK / 16; ++k) t5_mma_ts(tm + C::T_O + t * D, tm + C::T_P + t * C::PCOLS + 8 * k, b + 16 * (k % (NK / 16)), ID_O, k > 0 ? 1u : add);
                                 t5_commit(pv_done + t);
                             }
                             __syncwarp();
@@ -875,7 +896,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS, LIFT>::THREADS, 1)
                         const int ev = block_exp<VT, T::OFF_VS, NS>(tile, use);
                         if (lane == 0) s_exp[x & 7][1] = ev;
                     }
-                    convert_keys<KT, VT, NS>(tile, smem + C::OFF_K + buf * C::KHAT, e, cw, HALF);
+                    convert_keys<KT, VT, NS, FINE>(tile, smem + C::OFF_K + buf * C::KHAT, e, cw, HALF);
                 } else {
                     const int e = block_exp<VT, T::OFF_VS, NS>(tile, use);
                     convert_values<KT, VT, NS>(tile, smem + C::OFF_V + buf * C::VHAT, e, use, cw, HALF);
@@ -897,7 +918,8 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS, LIFT>::THREADS, 1)
             const int tile = (warp - C::SOFT0) >> 2, quarter = warp & 3;
             const int r = 32 * quarter + lane;  // row of the tile = lane of tensor memory
             const uint32_t trow = tm + (static_cast<uint32_t>(32 * quarter) << 16);
-            const uint32_t tS = trow + C::T_S + tile * NK, tP = trow + C::T_P + tile * (NK / 2), tO = trow + C::T_O + tile * D;
+            const uint32_t tS = trow + C::T_S + tile * NK, tP = trow + C::T_P + tile * C::PCOLS, tO = trow + C::T_O + tile * D;
+            const bool q_tmem = C::Q0_TMEM && tile == 0;
             ChunkWalk w = begin();
             int c0 = s_start[3], x = 0, done = 0;
             bool ok = true;
@@ -937,12 +959,12 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS, LIFT>::THREADS, 1)
                                     h[2 * e] = h2_as_u32(__floats2half2_rn(q4.x * up, q4.z * up));
                                     h[2 * e + 1] = h2_as_u32(__floats2half2_rn(q4.y * up, q4.w * up));
                                 }
-                                if (tile == 0) {
+                                if (q_tmem) {
                                     t5_st16(trow + C::T_Q + (p0 + d0) / 2, h);
                                 } else {
 #pragma unroll
                                     for (int e = 0; e < 4; ++e)
-                                        *reinterpret_cast<uint4 *>(smem + C::OFF_Q + core_at(r, p0 + d0 + 8 * e, D)) =
+                                        *reinterpret_cast<uint4 *>(smem + C::q_at(tile) + core_at(r, p0 + d0 + 8 * e, D)) =
                                             make_uint4(h[4 * e], h[4 * e + 1], h[4 * e + 2], h[4 * e + 3]);
                                 }
                             }
@@ -962,12 +984,12 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS, LIFT>::THREADS, 1)
                         if (__any_sync(0xffffffffu, off)) {
                             keep_branch();
                             const int k = off ? max(-120, min(120, 10 - (ex - 127))) : 0;
-                            if (tile == 0) t5_wait_st();
+                            if (q_tmem) t5_wait_st();
                             (void)stage(sign * __int_as_float((127 + k) << 23));
                             rs *= __int_as_float((127 - k) << 23);
                         }
                     }
-                    if (tile == 0)
+                    if (q_tmem)
                         t5_wait_st();
                     else
                         smem_to_async();
@@ -1023,14 +1045,19 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS, LIFT>::THREADS, 1)
                         const float base = (m_run == -CUDART_INF_F ? 0.f : m_run) - static_cast<float>(ev);
                         const float2 f2 = make_float2(f, f), nb2 = make_float2(-base, -base);
                         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                        uint32_t pw[NK / 2];
+                        uint32_t pw[NK / 2], pl[FINE ? NK / 2 : 1];  // weights, and what their rounding left
 #pragma unroll
                         for (int k = 0; k < NK / 2; ++k) {
                             float2 a = pair_fma(make_float2(s[2 * k], s[2 * k + 1]), f2, nb2);
                             a.x = chunk_ex2(a.x);
                             a.y = chunk_ex2(a.y);
                             sum[k & 1] = pair_add(sum[k & 1], a);
-                            pw[k] = h2_as_u32(__floats2half2_rn(a.x, a.y));
+                            const __half2 hi = __floats2half2_rn(a.x, a.y);
+                            pw[k] = h2_as_u32(hi);
+                            if constexpr (FINE) {
+                                const float2 f = __half22float2(hi);
+                                pl[k] = h2_as_u32(__floats2half2_rn(a.x - f.x, a.y - f.y));
+                            }
                         }
                         sum[0] = pair_add(sum[0], sum[1]);
                         l += (sum[0].x + sum[0].y) * __int_as_float((127 - ev) << 23);
@@ -1054,6 +1081,7 @@ __global__ void __launch_bounds__(ChunkCfg<KT, VT, NS, LIFT>::THREADS, 1)
                             }
                         }
                         t5_st32(tP, pw);
+                        if constexpr (FINE) t5_st32(tP + NK / 2, pl);
                         t5_wait_st();
                         t5_fence_before();
                         __syncwarp();
@@ -1181,7 +1209,8 @@ __global__ void __launch_bounds__(256)
 
 template <int KT, int VT, int NS, int DT, bool LIFT>
 cudaError_t launch_chunk_t(const PagedAttnParams &p, cudaStream_t stream) {
-    using C = ChunkCfg<KT, VT, NS, LIFT>;
+    constexpr bool FINE = chunk_fine<KT, DT>();
+    using C = ChunkCfg<KT, VT, NS, LIFT, FINE>;
     static bool configured[kPagedMaxDevices] = {};
     int dev = 0, sms = 0;
     cudaError_t e = paged_device(&dev, &sms);
@@ -1191,7 +1220,7 @@ cudaError_t launch_chunk_t(const PagedAttnParams &p, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
-    const ChunkWork work = chunk_work(p, sms, C::ROWS, C::D, nullptr);
+    const ChunkWork work = chunk_work(p, sms, C::ROWS, C::D, FINE, nullptr);
     // sequences of one launch: their prefix sums fit shared memory, their steps 2^30
     const long long fit = kPagedMaxSteps / chunk_seq_steps(p, C::ROWS);
     const int most = static_cast<int>(fit < kChunkMaxSeqs ? fit : kChunkMaxSeqs);
@@ -1199,7 +1228,7 @@ cudaError_t launch_chunk_t(const PagedAttnParams &p, cudaStream_t stream) {
     for (int b = 0; b < p.v.n_seqs; b += most) {
         const PagedAttnParams q = paged_some(p, b, most);
         if (LIFT) {
-            e = launch_dependent(paged_lift_kernel<KT, VT, NS>, dim3(sms * 4), 32 * kLiftWarps, 0, stream, q, work);
+            e = launch_dependent(paged_lift_kernel<KT, VT, NS, FINE>, dim3(sms * 4), 32 * kLiftWarps, 0, stream, q, work);
             if (e != cudaSuccess) return e;
         }
         e = launch_dependent(paged_chunk_kernel<KT, VT, NS, DT, LIFT>, dim3(sms), C::THREADS, C::SMEM, stream, q, work);
@@ -1213,7 +1242,7 @@ cudaError_t launch_chunk_t(const PagedAttnParams &p, cudaStream_t stream) {
 
 template <int DT>
 cudaError_t launch_chunk_dt(int type_k, int type_v, int D, const PagedAttnParams &p, cudaStream_t s) {
-    const bool lift = lift_blocks(p, D) > 0;
+    const bool lift = lift_blocks(p, D, type_k != KVQ_F16 && DT == KVQ_DT_F16) > 0;
 #define KVQ_CHUNK_CASE(KT_, VT_)                                                  \
     if (type_k == KT_ && type_v == VT_) {                                                            \
         if (D == kSlice) return lift ? launch_chunk_t<KT_, VT_, 1, DT, true>(p, s) : launch_chunk_t<KT_, VT_, 1, DT, false>(p, s);     \
