@@ -17,7 +17,7 @@
 // Products.  Keys and values are the A operands of mma.sync m16n8k16 (16 keys, or 16 values, by
 // 16) and the query rows its eight columns, so one instruction serves 16 keys x 8 rows without
 // waste, and the accumulators of O^T need four registers per 16 values.  Codes enter as f16
-// subnormals (a permute or a mask and no arithmetic); scales multiply S in fp32 and P in f16.
+// subnormals (a permute or a mask and no arithmetic; for fp32 activations as normal numbers); scales multiply S in fp32 and P in f16.
 // tcgen05 would need M = 128 query rows and the codes converted to f16 in shared memory, more
 // instructions per byte than this kernel issues in all.
 //
@@ -100,11 +100,35 @@ __device__ __forceinline__ uint32_t byte_perm0(uint32_t a) {
     asm("prmt.b32 %0, %1, 0, %2;\n" : "=r"(d) : "r"(a), "n"(SEL));
     return d;
 }
-// bytes 0, 2 / 1, 3 of a word of q8_0 codes (sign and magnitude) as f16 subnormals q 2^-24
-__device__ __forceinline__ uint32_t code8_02(uint32_t w) { return byte_perm0<0xA280u>(w) & 0x807f807fu; }
-__device__ __forceinline__ uint32_t code8_13(uint32_t w) { return byte_perm0<0xB391u>(w) & 0x807f807fu; }
+// Codes as f16 operands.  Plain: subnormals, by a permute or a mask alone.  EXACT (fp32 activations): one operation
+// more makes normal numbers, and 4-bit codes lose their offset, because sums of products of subnormals keep fewer
+// bits: 3e-6 to 1e-5 of the outputs' norm for 4-bit values (2e-7 to 9e-7 this way), nothing beside the rounding of a
+// 16-bit output but 4 to 18 times the error of plain fp32.
+//
+// bytes 0, 2 / 1, 3 of a word of q8_0 codes (sign and magnitude): q 2^-24, or EXACT q 2^-10
+template <bool EXACT>
+__device__ __forceinline__ uint32_t code8(uint32_t x) {
+    if constexpr (EXACT) return h2_as_u32(__hmul2(u32_as_h2(x & 0x807f807fu), __float2half2_rn(16384.0f)));
+    return x & 0x807f807fu;
+}
+template <bool EXACT>
+__device__ __forceinline__ uint32_t code8_02(uint32_t w) { return code8<EXACT>(byte_perm0<0xA280u>(w)); }
+template <bool EXACT>
+__device__ __forceinline__ uint32_t code8_13(uint32_t w) { return code8<EXACT>(byte_perm0<0xB391u>(w)); }
 constexpr uint32_t kLowNib = 0x000f000fu, kHighNib = 0x00f000f0u;
-constexpr float kUnit24 = 16777216.0f, kUnit20 = 1048576.0f;
+// nibbles of q4_0 codes: c 2^-24 and 16 c 2^-24, or EXACT the integers c - 8
+template <bool EXACT>
+__device__ __forceinline__ uint32_t code4_low(uint32_t x) {
+    if constexpr (EXACT) return h2_as_u32(__hsub2(u32_as_h2((x & kLowNib) | 0x64006400u), __float2half2_rn(1032.0f)));
+    return x & kLowNib;
+}
+template <bool EXACT>
+__device__ __forceinline__ uint32_t code4_high(uint32_t x) {
+    if constexpr (EXACT)
+        return h2_as_u32(__hfma2(u32_as_h2((x & kHighNib) | 0x64006400u), __float2half2_rn(0.0625f), __float2half2_rn(-72.0f)));
+    return x & kHighNib;
+}
+constexpr float kUnit24 = 16777216.0f, kUnit20 = 1048576.0f, kUnit10 = 1024.0f;
 
 // d = A B + C with C = (c0, c1) in every row
 __device__ __forceinline__ void mma_16816_c(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1) {
@@ -119,7 +143,7 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) { return h2_as_
 template <int KT, int NS, bool QLO>
 struct QueryFrags {
     uint32_t hi[NS * 8][2], lo[QLO ? NS * 8 : 1][2];
-    float corr[KT == KVQ_Q4_0 ? NS * 4 : 1][2];  // -8 times the sum of q over each block, in accumulator units
+    float corr[KT == KVQ_Q4_0 && !QLO ? NS * 4 : 1][2];  // -8 times the sum of q over each block, in accumulator units
     float scale[2];                              // raw scores (accumulator units) to log2 units, >= 0
 };
 
@@ -141,11 +165,12 @@ __device__ __forceinline__ void load_queries(QueryFrags<KT, NS, QLO> &f, const t
     k = max(-120, min(120, k));
     // a negative scale goes to the query, so that the largest raw score of a row is its largest score
     const float up = __int_as_float(((127 + k) << 23) | (scale < 0.f ? 0x80000000 : 0)), down = __int_as_float((127 - k) << 23);
-    const float rs = fabsf(scale) * kSplitLog2e * down * (KT == KVQ_F16 ? 1.f : (KT == KVQ_Q4_0 ? kUnit20 : kUnit24));
+    constexpr float unit = KT == KVQ_F16 ? 1.f : KT == KVQ_Q4_0 ? (QLO ? 1.f : kUnit20) : (QLO ? kUnit10 : kUnit24);
+    const float rs = fabsf(scale) * kSplitLog2e * down * unit;
 #pragma unroll
     for (int c = 0; c < NS * 8; ++c) {
         // low nibbles count 1 and high nibbles 16 of the accumulator's unit
-        const float u = (KT == KVQ_Q4_0 && (c & 1) == 0) ? up * 16.f : up;
+        const float u = (KT == KVQ_Q4_0 && !QLO && (c & 1) == 0) ? up * 16.f : up;
         const float a = x[c].x * u, b = x[c].y * u, e = x[c].z * u, d = x[c].w * u;
         // k = 2j, 2j + 1 of the MMA are values 0, 2 of the four and 2j + 8, 2j + 9 values 1, 3 (the
         // order in which the key codes' bytes come out of a word)
@@ -157,7 +182,7 @@ __device__ __forceinline__ void load_queries(QueryFrags<KT, NS, QLO> &f, const t
             f.lo[c][1] = pack_half2(b - h1.x, d - h1.y);
         }
     }
-    if constexpr (KT == KVQ_Q4_0) {
+    if constexpr (KT == KVQ_Q4_0 && !QLO) {
         // the score of a key whose codes are all 8, block by block: what the offset adds
         const uint32_t lo8[4] = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
         const uint32_t hi8[4] = {0x00800080u, 0x00800080u, 0x00800080u, 0x00800080u};
@@ -166,10 +191,6 @@ __device__ __forceinline__ void load_queries(QueryFrags<KT, NS, QLO> &f, const t
             float acc[4];
             mma_16816_z(acc, lo8, f.hi[2 * b][0], f.hi[2 * b][1]);
             mma_16816(acc, hi8, f.hi[2 * b + 1][0], f.hi[2 * b + 1][1]);
-            if constexpr (QLO) {
-                mma_16816(acc, lo8, f.lo[2 * b][0], f.lo[2 * b][1]);
-                mma_16816(acc, hi8, f.lo[2 * b + 1][0], f.lo[2 * b + 1][1]);
-            }
             f.corr[b][0] = -acc[0];
             f.corr[b][1] = -acc[1];
         }
@@ -189,9 +210,9 @@ __device__ __forceinline__ void tile_s(const uint8_t *kc, const uint8_t *ks, con
         for (int b = 0; b < NS * 4; ++b) {
             const uint4 w0 = lds128(kc + (2 * b) * 512 + lane * 16), w1 = lds128(kc + (2 * b + 1) * 512 + lane * 16);
             const uint32_t a0[4] = {w0.x, w1.x, w0.y, w1.y}, a1[4] = {w0.z, w1.z, w0.w, w1.w};
-            if (b == 0) {
-                mma_16816_z(acc[0], a0, f.hi[0][0], f.hi[0][1]);
-                mma_16816_z(acc[1], a1, f.hi[1][0], f.hi[1][1]);
+            if (b == 0 || QLO) {  // QLO: short chains of products, summed in fp32
+                mma_16816_z(acc[0], a0, f.hi[2 * b][0], f.hi[2 * b][1]);
+                mma_16816_z(acc[1], a1, f.hi[2 * b + 1][0], f.hi[2 * b + 1][1]);
             } else {
                 mma_16816(acc[0], a0, f.hi[2 * b][0], f.hi[2 * b][1]);
                 mma_16816(acc[1], a1, f.hi[2 * b + 1][0], f.hi[2 * b + 1][1]);
@@ -199,10 +220,13 @@ __device__ __forceinline__ void tile_s(const uint8_t *kc, const uint8_t *ks, con
             if constexpr (QLO) {
                 mma_16816(acc[0], a0, f.lo[2 * b][0], f.lo[2 * b][1]);
                 mma_16816(acc[1], a1, f.lo[2 * b + 1][0], f.lo[2 * b + 1][1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[i] = (b == 0 ? 0.f : s[i]) + (acc[0][i] + acc[1][i]);
             }
         }
+        if constexpr (!QLO)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = acc[0][i] + acc[1][i];
+            for (int i = 0; i < 4; ++i) s[i] = acc[0][i] + acc[1][i];
     } else {
         s[0] = s[1] = s[2] = s[3] = 0.f;
         // key g is member g % 2 of the pairs of lane group g / 2, key g + 8 member 2 + g % 2
@@ -220,16 +244,18 @@ __device__ __forceinline__ void tile_s(const uint8_t *kc, const uint8_t *ks, con
                 float acc[4];
                 if constexpr (KT == KVQ_Q8_0) {
                     const uint4 w = lds128(kcs + b * 512 + lane * 16);
-                    a0[0] = code8_02(w.x), a0[1] = code8_02(w.z), a0[2] = code8_13(w.x), a0[3] = code8_13(w.z);
-                    a1[0] = code8_02(w.y), a1[1] = code8_02(w.w), a1[2] = code8_13(w.y), a1[3] = code8_13(w.w);
+                    a0[0] = code8_02<QLO>(w.x), a0[1] = code8_02<QLO>(w.z), a0[2] = code8_13<QLO>(w.x), a0[3] = code8_13<QLO>(w.z);
+                    a1[0] = code8_02<QLO>(w.y), a1[1] = code8_02<QLO>(w.w), a1[2] = code8_13<QLO>(w.y), a1[3] = code8_13<QLO>(w.w);
                     mma_16816_z(acc, a0, f.hi[c][0], f.hi[c][1]);
                 } else {
                     if ((b & 1) == 0) w4 = lds128(kcs + (b >> 1) * 512 + lane * 16);
                     const uint32_t u = (b & 1) ? w4.z : w4.x, w = (b & 1) ? w4.w : w4.y, u8 = u >> 8, w8 = w >> 8;
-                    a0[0] = u & kLowNib, a0[1] = w & kLowNib, a0[2] = u8 & kLowNib, a0[3] = w8 & kLowNib;
-                    a1[0] = u & kHighNib, a1[1] = w & kHighNib, a1[2] = u8 & kHighNib, a1[3] = w8 & kHighNib;
-                    const int bi = sl * 4 + b;
-                    mma_16816_c(acc, a0, f.hi[c][0], f.hi[c][1], f.corr[bi][0], f.corr[bi][1]);
+                    a0[0] = code4_low<QLO>(u), a0[1] = code4_low<QLO>(w), a0[2] = code4_low<QLO>(u8), a0[3] = code4_low<QLO>(w8);
+                    a1[0] = code4_high<QLO>(u), a1[1] = code4_high<QLO>(w), a1[2] = code4_high<QLO>(u8), a1[3] = code4_high<QLO>(w8);
+                    if constexpr (QLO)
+                        mma_16816_z(acc, a0, f.hi[c][0], f.hi[c][1]);
+                    else
+                        mma_16816_c(acc, a0, f.hi[c][0], f.hi[c][1], f.corr[sl * 4 + b][0], f.corr[sl * 4 + b][1]);
                 }
                 mma_16816(acc, a1, f.hi[c + 1][0], f.hi[c + 1][1]);
                 if constexpr (QLO) {
@@ -268,9 +294,9 @@ __device__ __forceinline__ bool big_scales(const uint8_t *vs, int valid) {
 
 // O^T += V^T P^T for one tile.  ph / pl: weights of keys (2j, 2j + 1) and (2j + 8, 2j + 9) of row g;
 // mab / mcd: masks of those keys (rows past the sequence's end may hold any bits).  o[2b], o[2b + 1]:
-// values 32b + 2g, + 1 and 32b + 16 + 2g, + 1 of rows 2j, 2j + 1.  For q4_0, corr row b collects
-// the sum of weight x scale of block b, by which 8 has been added to every code.
-template <int VT, int NS, bool PLO, bool MASK>
+// values 32b + 2g, + 1 and 32b + 16 + 2g, + 1 of rows 2j, 2j + 1.  For q4_0 without EXACT, corr row b
+// collects the sum of weight x scale of block b, by which 8 has been added to every code.
+template <int VT, int NS, bool PLO, bool EXACT, bool MASK>
 __device__ __forceinline__ void tile_o(const uint8_t *vc, const uint8_t *vs, const uint32_t (&ph)[2], const uint32_t (&pl)[2],
                                        uint32_t mab, uint32_t mcd, float (&o)[NS * 8][4], float (&corr)[4]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, j = lane & 3;
@@ -314,17 +340,19 @@ __device__ __forceinline__ void tile_o(const uint8_t *vc, const uint8_t *vs, con
                 uint32_t a0[4], a1[4];
                 if constexpr (VT == KVQ_Q8_0) {
                     const uint4 w = lds128(vcs + b * 512 + lane * 16);
-                    a0[0] = code8_02(w.x), a0[1] = code8_02(w.y), a0[2] = code8_13(w.x), a0[3] = code8_13(w.y);
-                    a1[0] = code8_02(w.z), a1[1] = code8_02(w.w), a1[2] = code8_13(w.z), a1[3] = code8_13(w.w);
+                    a0[0] = code8_02<EXACT>(w.x), a0[1] = code8_02<EXACT>(w.y), a0[2] = code8_13<EXACT>(w.x), a0[3] = code8_13<EXACT>(w.y);
+                    a1[0] = code8_02<EXACT>(w.z), a1[1] = code8_02<EXACT>(w.w), a1[2] = code8_13<EXACT>(w.z), a1[3] = code8_13<EXACT>(w.w);
                 } else {
                     if ((b & 1) == 0) w4 = lds128(vcs + (b >> 1) * 512 + lane * 16);
                     const uint32_t u = (b & 1) ? w4.z : w4.x, w = (b & 1) ? w4.w : w4.y, u8 = u >> 8, w8 = w >> 8;
-                    a0[0] = u & kLowNib, a0[1] = w & kLowNib, a0[2] = u8 & kLowNib, a0[3] = w8 & kLowNib;
-                    a1[0] = u & kHighNib, a1[1] = w & kHighNib, a1[2] = u8 & kHighNib, a1[3] = w8 & kHighNib;
-                    const uint32_t one = g == sl * 4 + b ? 0x3c003c00u : 0u;  // row b of the collecting operand
-                    const uint32_t ac[4] = {one, 0u, one, 0u};
-                    mma_16816(corr, ac, b0, b1);
-                    if constexpr (PLO) mma_16816(corr, ac, l0, l1);
+                    a0[0] = code4_low<EXACT>(u), a0[1] = code4_low<EXACT>(w), a0[2] = code4_low<EXACT>(u8), a0[3] = code4_low<EXACT>(w8);
+                    a1[0] = code4_high<EXACT>(u), a1[1] = code4_high<EXACT>(w), a1[2] = code4_high<EXACT>(u8), a1[3] = code4_high<EXACT>(w8);
+                    if constexpr (!EXACT) {
+                        const uint32_t one = g == sl * 4 + b ? 0x3c003c00u : 0u;  // row b of the collecting operand
+                        const uint32_t ac[4] = {one, 0u, one, 0u};
+                        mma_16816(corr, ac, b0, b1);
+                        if constexpr (PLO) mma_16816(corr, ac, l0, l1);
+                    }
                 }
                 mma_16816(o[t], a0, b0, b1);
                 mma_16816(o[t + 1], a1, b0, b1);
@@ -512,10 +540,10 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 8);
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 16);
         }
-        if constexpr (VT != KVQ_F16) {
+        if constexpr (VT == KVQ_Q8_0 || (VT == KVQ_Q4_0 && !C::QLO)) {
 #pragma unroll
             for (int t = 0; t < NS * 8; ++t) {
-                const float unit = (VT == KVQ_Q4_0 && (t & 1)) ? kUnit20 : kUnit24;
+                const float unit = (VT == KVQ_Q4_0 && (t & 1)) ? kUnit20 : (C::QLO ? kUnit10 : kUnit24);
                 float c0 = 0.f, c1 = 0.f;
                 if constexpr (VT == KVQ_Q4_0) {  // row t / 2 of corr: lanes 4 (t / 2) + j
                     c0 = 8.f * __shfl_sync(0xffffffffu, corr[0], (t >> 1) * 4 + j);
@@ -778,9 +806,9 @@ __global__ void __launch_bounds__(SplitCfg<KT, VT, NS, DT>::THREADS, 1)
                 if (cut) {
                     keep_branch();
                     auto mask = [&](int k) { return k + 1 < valid[i] ? 0xffffffffu : (k < valid[i] ? 0x0000ffffu : 0u); };
-                    tile_o<VT, NS, C::PLO, true>(tv, tvs, ph, pl, mask(2 * j), mask(2 * j + 8), o, corr);
+                    tile_o<VT, NS, C::PLO, C::QLO, true>(tv, tvs, ph, pl, mask(2 * j), mask(2 * j + 8), o, corr);
                 } else {
-                    tile_o<VT, NS, C::PLO, false>(tv, tvs, ph, pl, 0u, 0u, o, corr);
+                    tile_o<VT, NS, C::PLO, C::QLO, false>(tv, tvs, ph, pl, 0u, 0u, o, corr);
                 }
             }
             __syncwarp();  // the slot has been read

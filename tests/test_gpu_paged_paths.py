@@ -141,3 +141,49 @@ def test_expanded_tables_are_refused(kvq):
     with pytest.raises(kvq.KvqError) as e:
         b.cache.attention(b.queries(4, "bf16"), row, b.lens_t)
     assert e.value.status == 1
+
+
+@pytest.mark.parametrize("pair", [("q8_0", "q4_0"), ("q4_0", "q4_0")])
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("new", [1, 5])
+def test_fp32_of_4_bit_pages_without_the_offset(kvq, pair, d, new):
+    """fp32 outputs of 4-bit rows: the codes' offset adds no error of its own (the bounds of bounds() alone)."""
+    lens = [700, 64, 3000]
+    b = Batch(kvq, lens, [new] * 3, d=d, pair=pair, page=48, seed=15)
+    q = b.queries(8, "f32")
+    out = b.cache.attention(q, b.table, b.lens_t, cu_q=b.cu, max_q=new)
+    at = 0
+    for i, a in enumerate(lens):
+        k, v = b.values(i)
+        o, _, av, qk = attend(q[at:at + new], k, v, 1 / math.sqrt(d))
+        tol, _ = bounds(o, av, qk, "f32", a, d, False)
+        assert ((out[at:at + new].double() - o).abs() <= tol).all(), i
+        # and in the norm, where roundings of 2^-22 of the weights and 2^-24 a step do not add up one way
+        # (codes summed as subnormals, 0 .. 15, and the offset taken off after it gave 4.5e-6)
+        err = (out[at:at + new].double() - o).norm() / o.norm()
+        assert err < 2.0 ** -18, (i, float(err))
+        at += new
+
+
+@pytest.mark.parametrize("pair", PAIRS[1:])
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("lift", [True, False])
+def test_f16_chunks_keep_their_scores(kvq, pair, d, lift):
+    """f16 activations over quantised pages: keys count as hi + lo, so the scores' part of the bound is 2^-20,
+    not 2^-11 (lse has no other rounding of 16 bits)."""
+    lens, new, page = [900, 130], [70, 130], 64
+    b = Batch(kvq, lens, new, d=d, pair=pair, page=page, seed=16)
+    width = b.table.shape[1] if lift else (1 << 21) // page
+    wide = torch.full((2, width), -9, dtype=torch.int32, device="cuda")
+    wide[:, :b.table.shape[1]] = b.table
+    q = b.queries(8, "f16")
+    out, lse = b.cache.attention(q, wide, b.lens_t, cu_q=b.cu, max_q=130, return_lse=True)
+    at = 0
+    for i, (a, m) in enumerate(zip(lens, new)):
+        k, v = b.values(i)
+        o, z, av, qk = attend(q[at:at + m], k, v, 1 / math.sqrt(d))
+        tol, ltol = bounds(o, av, qk, "f16", a, d, False)
+        assert ((out[at:at + m].double() - o).abs() <= tol).all(), i
+        assert ((lse[at:at + m].double() - z).abs() <= ltol).all(), i
+        at += m
+    assert b.cache.read_error() == 0
