@@ -575,9 +575,24 @@ KVQ_API kvq_status kvq_paged_gather(const kvq_paged *cache, const kvq_paged_batc
  *   out  : [n_tokens][n_q_heads][D] of type dtype, contiguous; a token that attends to nothing
  *          gets 0
  *   lse  : fp32 [n_tokens][n_q_heads], natural log (-inf where nothing is attended), or NULL
- *   workspace: kvq_paged_attention_workspace_size bytes for the same batch sizes; needs no
- *          initialisation and keeps nothing between calls.
- * n_q_heads: a multiple of Hkv.  fp32 queries: max_q at most KVQ_MAX_VERIFY_QUERIES.
+ *   workspace: kvq_paged_attention_workspace_size bytes for the same batch sizes (fewer give
+ *          KVQ_ERR_SCRATCH); needs no initialisation and keeps nothing between calls.  Two calls
+ *          that may run at the same time, replays of two captured graphs among them, need one
+ *          each.  With many queries it also holds the keys and values of the sequences as 16-bit
+ *          operands, unless the batch's bounds would make them more than 2 GiB: then they are
+ *          made inside the kernel, so a tight max_len serves speed.
+ * n_q_heads: a multiple of Hkv, at most 65535.  fp32 queries: max_q at most
+ * KVQ_MAX_VERIFY_QUERIES.  q, out, lse, workspace and pool must not overlap.
+ * Sizes: (blocks of 64 positions in max_len) x (units of 128 or 256 query rows in max_q, or of 8
+ * where few) x Hkv at most 2^30 and max_len below 2^31 - 1024, else KVQ_ERR_UNSUPPORTED.
+ * Rounding: scores, maxima and sums in fp32.  fp32: as fp32 arithmetic.  f16 and bf16: beside the
+ * output's own rounding at most three of 2^-11 (key, weight, value); f16 over quantised types
+ * keeps keys and weights to 2^-20.  Results do not depend on timing: no atomics on data.
+ * Values that are not finite: a key that is infinite or NaN reaches the tokens that attend to it
+ * alone.  A V row that is infinite or NaN also reaches tokens of the same call up to 63
+ * positions before it (0 x inf in a tile's product); rows past lens[b] reach nothing.
+ * Launches: one or two for few queries per sequence, three for many, both where a batch has both.
+ * A wait that passes two seconds sets KVQ_DEVERR_TIMEOUT and its CTA's rows are not written.
  */
 KVQ_API kvq_status kvq_paged_attention_workspace_size(const kvq_paged *cache, const kvq_paged_batch *batch,
                                                       int32_t n_q_heads, kvq_dtype dtype, size_t *bytes);

@@ -437,6 +437,7 @@ def _need(ok, what):
 
 def paged_size(n_pages, page_size, n_kv_heads, head_dim, type_k, type_v):
     """(pool_bytes, state_bytes) of a paged cache (kvq_paged_size); pure host arithmetic."""
+    _need(max(n_pages, page_size, n_kv_heads, head_dim) < 2**31, "32-bit sizes")  # ctypes would wrap them
     d = PagedDesc(n_pages, page_size, n_kv_heads, head_dim, _tid(type_k), _tid(type_v))
     pb, sb = ctypes.c_size_t(), ctypes.c_size_t()
     _check(lib.kvq_paged_size(ctypes.byref(d), ctypes.byref(pb), ctypes.byref(sb)), "kvq_paged_size")
@@ -458,6 +459,9 @@ class Rope:
         j = torch.arange(rot_dim // 2, dtype=torch.float64, device=device or "cuda")
         a = torch.arange(n_positions, dtype=torch.float64, device=j.device)[:, None] * base ** (-2.0 * j / rot_dim)
         return cls(torch.cat([a.cos(), a.sin()], -1).float().contiguous(), interleaved)
+
+
+_MAX_LEN = 2**31 - 1025  # longest sequence of a paged call
 
 
 class PagedCache:
@@ -512,8 +516,11 @@ class PagedCache:
             if max_q is None:
                 max_q = max(1, n_tokens)
         width = shape[1]
+        if max_len is None:
+            max_len = min(width * self.page_size, _MAX_LEN)
+        _need(max_len < 2**31 and max_q < 2**31, "max_len and max_q: 32-bit sizes")  # ctypes would wrap them
         # one row has any stride; rows that overlap (an expanded table) are refused by the call itself
-        return PagedBatch(n_seqs, n_tokens, max_q, width * self.page_size if max_len is None else max_len, cu, lens.data_ptr(),
+        return PagedBatch(n_seqs, n_tokens, max_q, max_len, cu, lens.data_ptr(),
                           block_table.data_ptr(), width, strides[0] if n_seqs > 1 else max(width, strides[0]))
 
     def _rows(self, t, heads, what, dtype=None):
@@ -634,6 +641,7 @@ class PagedCache:
 
     def workspace_bytes(self, n_seqs, n_tokens, n_q_heads, max_len, max_q=1, dtype=torch.bfloat16) -> int:
         """Workspace of attention calls of these sizes (max_q tokens at most per sequence)."""
+        _need(max(n_seqs, n_tokens, max_len, max_q) < 2**31, "32-bit sizes")
         width = -(-max_len // self.page_size)
         # the arrays' contents do not matter: any aligned address stands for them
         batch = PagedBatch(n_seqs, n_tokens, max_q, max_len, 16 if max_q > 1 else 0, 16, 16, max(1, width), max(1, width))

@@ -2,6 +2,11 @@
 // quantisation on the way in) and gather (values out).
 #include "kvq_paged.cuh"
 
+// Bound by memory for chunks and by latency for single tokens (us on a GB300, of measured copy bandwidth):
+// append of 10017 tokens in 3 chunks, 8 KV and 40 query heads of 128 rotated, bf16 to q4_0, 69 us (3.9 TB/s, 57 %:
+// half the grid quantises, bound by its instructions, half rotates queries, bound by memory); 4096 tokens, 2 and 16
+// heads of 256, fp32 to q8_0, 39 us (4.0 TB/s); one token 7.1 us, 64 tokens 8.2 us.  Gather of 65536 positions,
+// q8_0 / q4_0 to bf16: 67 us (5.7 TB/s, 83 %); five short sequences 4.4 us.
 namespace kvq {
 namespace {
 

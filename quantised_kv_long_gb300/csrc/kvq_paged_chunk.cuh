@@ -9,18 +9,24 @@
 // per SM), so ragged and causal work is even whatever the lengths.  A unit cut by a span boundary
 // leaves pieces (m, l, o) in the workspace, which a second kernel merges.
 //
-// A step, by warps: warp 0 streams the block's tile records into a ring; half of the converter warps
-// turn key codes into the f16 operand K^ (keys x D) in shared memory, the other half value codes into
-// V^ (D x keys), once for all rows of the unit; warp 1 issues S = Q K^T, warps 2 and 3 issue
-// O += P V^ of a tile each; four warps per tile hold one row per thread:
-// running maximum, weights, P into tensor memory, and the rescale of O when the maximum moves by more
-// than kChunkDrift.  S of the next block is computed while the softmax of this one runs (S and P have
-// their own columns).
+// A step, by warps: warp 0 streams the block's f16 operands K^ (keys x D) and V^ (D x keys) into a ring;
+// S = Q K^T of each tile is issued by a warp of its own (1, and 2 for the second tile), O += P V^ by one
+// more; four warps per tile hold one row per thread: running maximum, weights, P into tensor memory, and
+// the rescale of O when the maximum moves by more than kChunkDrift.  S of the next block is computed
+// while the softmax of this one runs (S and P have their own columns).
 //
-// Lifted.  Converting costs about as many instructions as the softmax of 256 rows, once per unit; so a kernel
-// before this one makes the operands of every block once, in the order the MMA reads them, and the chunk
-// kernel streams them from the workspace (LIFT) without converters: 32 KB per step and head of 128 instead
-// of 9 to 32 KB of codes.  Where that workspace would be too large (kLiftBytes) the converters run inside.
+// Lifted.  Converting codes costs about as many instructions as the softmax of 256 rows, once per unit; so a
+// kernel before this one makes the operands of every block once, in the order the MMA reads them, and the
+// chunk kernel streams them from the workspace (LIFT): 32 KB per step and head of 128 instead of 9 to 32 KB of
+// codes.  Where that workspace would be too large (kLiftBytes) warp 0 streams tile records and eight converter
+// warps make the operands in shared memory.
+//
+// Measured (4096 bf16 queries, 40 heads over 8, the end of 16384 positions, q4_0): 840 us, 1430 TFLOP/s, of it
+// lift 15 and merge 22 us; a step of 256 rows takes 1710 cycles, its products 1160 (N = 64: 32 cycles with
+// Q in tensor memory, 48 from shared memory; N = 128: 64), and waits for the softmax of its rows (700 cycles of
+// arithmetic, 300 of tensor-memory loads and stores, the rest barriers).  256-wide, 128 rows: 1500 cycles, products
+// 1024 (f16 over quantised pages, as pairs: about 2300 and 2048).  Tried and dropped: two buffers of P (256-wide the same, 128-wide 898 us, for Q then leaves tensor
+// memory), a warp per tile for O, test_wait before try_wait, spinning waits (worse).
 //
 // Orders.  The values of K^ and Q sit in the order 0, 2, 1, 3 within each four (as the bytes of a code
 // word come out), and the rows of V^ (columns of O) in the order 0, 2, .., 14, 1, 3, .., 15 within each

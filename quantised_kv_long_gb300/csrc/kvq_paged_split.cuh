@@ -21,6 +21,11 @@
 // tcgen05 would need M = 128 query rows and the codes converted to f16 in shared memory, more
 // instructions per byte than this kernel issues in all.
 //
+// Measured (bf16 or as said, 8 KV heads of 128, 40 query heads): 16 sequences of 8192 to 65536 positions, q8_0 / q4_0,
+// f16 queries, 133 us (5.6 TB/s, 83 % of measured copy bandwidth, bound by memory and the instructions of its 12
+// warps alike); one of 131072, q4_0, 44 us (3.4 TB/s: 10 us of launches, sums and merge, then 4 instructions per
+// byte at 46 % issue); one of 513 positions 8.7 us; 4 of 4095 to 65535, 2 KV heads of 256, q8_0, fp32, 36 us.
+//
 // Rounding.  A query row is scaled by a power of two to a largest value of 2^10 .. 2^11, so that
 // f16 holds every 16-bit input; fp32 queries keep a second f16 part (hi + lo).  Weights are f16
 // for bf16 outputs (2^-11 beside the output's 2^-8) and hi + lo pairs for f16 and fp32 outputs.

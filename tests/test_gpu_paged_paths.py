@@ -187,3 +187,22 @@ def test_f16_chunks_keep_their_scores(kvq, pair, d, lift):
         assert ((lse[at:at + m].double() - z).abs() <= ltol).all(), i
         at += m
     assert b.cache.read_error() == 0
+
+
+def test_lengths_past_32_bits(kvq):
+    """A table that stands for more positions than 32 bits count: the default bound is cut, a given one refused."""
+    page, width = 1 << 16, 1 << 15
+    cache = kvq.PagedCache(2, page, 1, 128, "q4_0", "q4_0")
+    table = torch.full((1, width), 1, dtype=torch.int32, device="cuda")
+    x = torch.randn((3, 1, 128), device="cuda")
+    cu = dev([0, 3])
+    cache.append(x, x, table, dev([3]), cu_q=cu, max_q=3)
+    k, _ = cache.gather(table, dev([3]), 3, cu_q=cu, max_q=3, dtype=torch.float32)
+    assert np.array_equal(k.cpu().numpy().astype(np.float64), stored("q4_0", x.cpu().numpy()))
+    assert cache.read_error() == 0
+    with pytest.raises(ValueError):
+        cache.append(x, x, table, dev([3]), cu_q=cu, max_q=3, max_len=2 ** 32 + 16)
+    with pytest.raises(ValueError):
+        cache.attention(x, table, dev([3]), cu_q=cu, max_q=2 ** 32 + 3)
+    with pytest.raises(ValueError):
+        cache.workspace_bytes(1, 2 ** 32 + 1, 1, 64)

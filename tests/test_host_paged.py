@@ -184,3 +184,9 @@ def test_lengths_near_32_bits_are_refused():
         b = batch(max_len=max_len, table_width=2**28, table_stride=2**28)
         assert L.kvq_paged_gather(ctypes.byref(h), ctypes.byref(b), FAKE, FAKE, 0, None) == status
         assert L.kvq_paged_attention_workspace_size(ctypes.byref(h), ctypes.byref(b), 4, 0, ctypes.byref(sz)) == status
+
+
+def test_sizes_past_32_bits_do_not_wrap():
+    for desc in ((2**32 + 1, 16, 2, 128), (4, 2**32 + 16, 2, 128), (4, 16, 2**32 + 2, 128), (4, 16, 2, 2**32 + 128)):
+        with pytest.raises(ValueError):
+            kvq.paged_size(*desc, "q8_0", "q8_0")
