@@ -360,7 +360,7 @@ struct ChunkCfg {
     // Q of tile 0 is in tensor memory where there is room, of the others in shared memory
     static constexpr bool Q0_TMEM = !(FINE && NT == 2);
     static constexpr int QSM = (NT - (Q0_TMEM ? 1 : 0)) * M * D * 2;
-    static constexpr int LIMIT = 232448 - 3072;          // of the CTA's shared memory, barriers and statics kept back
+    static constexpr int LIMIT = 224 * 1024;             // of the CTA's 227 KB, the rest for barriers and statics
     // operand buffers: all that fit when lifted, else two of each, or one where two raw stages would not fit
     static constexpr int STAGE = LIFT ? 1 : TILES * T::BYTES;
     static constexpr int KB = LIFT ? (LIMIT - QSM) / IMAGE : (FINE && NS == 2 ? 1 : 2);

@@ -206,3 +206,52 @@ def test_lengths_past_32_bits(kvq):
         cache.attention(x, table, dev([3]), cu_q=cu, max_q=2 ** 32 + 3)
     with pytest.raises(ValueError):
         cache.workspace_bytes(1, 2 ** 32 + 1, 1, 64)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("hkv,hq", [(1, 128), (3, 300), (2, 2)])
+def test_many_and_single_heads_per_kv_head(kvq, hkv, hq, dtype):
+    """128, 100 and 1 query heads per KV head: one token fills the chunk kernel's rows, or 57 tokens do."""
+    lens, new = [333, 90, 70, 1, 0], [3, 90, 1, 1, 2]
+    b = Batch(kvq, lens, new, hkv=hkv, pair=("q8_0", "q4_0"), page=32, seed=23, pad=4)
+    q = b.queries(hq, dtype)
+    out, lse = torch.full_like(q, 5.0), None
+    out, lse = b.cache.attention(q, b.table, b.lens_t, cu_q=b.cu, max_q=90, return_lse=True, out=out)
+    b.check(q, dtype, out, lse)
+    assert bool((out[b.n:] == 5.0).all())
+    assert b.cache.read_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_one_sequence_of_any_tokens_in_a_captured_call(kvq, dtype):
+    """A captured call of one sequence with a bound of 96 tokens, replayed for 96, 1, 0 and 17 of them; twice the
+    same bits."""
+    b = Batch(kvq, [400], [96], pair=("q8_0", "q8_0"), page=64, seed=24)
+    q = b.queries(8, dtype)
+    lens, cu = b.lens_t.clone(), b.cu.clone()
+    out = torch.zeros_like(q)
+    ws = torch.empty(b.cache.workspace_bytes(1, 96, 8, b.table.shape[1] * 64, 96, q.dtype), dtype=torch.uint8, device="cuda")
+    run = lambda: b.cache.attention(q, b.table, lens, cu_q=cu, max_q=96, out=out, workspace=ws)  # noqa: E731
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    k, v = b.values(0)
+    for n, length in ((96, 400), (1, 400), (0, 0), (17, 17), (96, 130), (2, 1)):
+        lens.fill_(length)
+        cu.copy_(dev([0, n]))
+        got = []
+        for _ in range(2):
+            out.fill_(3.0)
+            ws.fill_(0xff)  # nothing is kept from a call to the next
+            g.replay()
+            torch.cuda.synchronize()
+            got.append(out.clone())
+        assert torch.equal(got[0], got[1])
+        o, _, av, qk = attend(q[:n], k[:length], v[:length], 1 / math.sqrt(128))
+        if n:
+            tol, _ = bounds(o, av, qk, dtype, length, 128, True)
+            assert ((got[0][:n].double() - o).abs() <= tol).all(), (n, length)
+        assert bool((got[0][n:] == 3.0).all()), (n, length)
+    assert b.cache.read_error() == 0
